@@ -186,7 +186,7 @@ def _adamw(c, seed):
         s["m"], s["v"] = m, v
     if own:
         import mixture_experts_lora_b200 as ml
-        opt = ml.AdamW(s["params"], lr=HYPER["lr"], betas=(HYPER["b1"], HYPER["b2"]), eps=HYPER["eps"],
+        opt = ml.AdamW(s["params"], s["grads"], lr=HYPER["lr"], betas=(HYPER["b1"], HYPER["b2"]), eps=HYPER["eps"],
                        weight_decay=HYPER["wd"], state_bits=c["bits"], master_weights=c["master"])
         opt.exp_avg.copy_(s["m"])
         opt.exp_avg_sq.copy_(s["v"])
@@ -395,7 +395,7 @@ def _own_balance(s):
 
 def _own_adamw(s):
     o = s["opt"]
-    o.step(s["grads"])
+    o.step()
     return _adamw_out(s, s["p"], o.exp_avg, o.exp_avg_sq, o.exp_avg_scale, o.exp_avg_sq_scale, o.master, o.steps)
 
 
