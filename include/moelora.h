@@ -69,7 +69,8 @@ typedef enum {
   MOE_ERR_UNSUPPORTED = 2,   /* shape outside the supported set above */
   MOE_ERR_WORKSPACE = 3,     /* ws_bytes smaller than moe_workspace_bytes() */
   MOE_ERR_CUDA = 4,          /* a CUDA runtime call or launch failed */
-  MOE_ERR_DEVICE_INDEX = 5,  /* device-detected: expert id outside [0, E) */
+  MOE_ERR_DEVICE_INDEX = 5,  /* device-detected: expert or adapter id out of range, or sequence
+                                offsets that decrease or leave [0, T] */
   MOE_ERR_TIMEOUT = 6,       /* device-detected: a bounded wait expired */
   MOE_ERR_DEVICE_CHECK = 7   /* device-detected: moe_check_permutation() found a broken invariant */
 } moe_status_t;
@@ -270,6 +271,120 @@ moe_status_t moe_router_backward(const moe_bf16_t* dY, const moe_bf16_t* Y_sorte
                                  const int32_t* topk_ids, const float* topk_w,
                                  const int32_t* pair_pos, int64_t T, int32_t k, int32_t E,
                                  int32_t m, float* dlogits, void* stream);
+
+/* Balance loss of the router, per sequence, with the per-expert counts.  Sequence s is the
+ * rows [seq_offsets[s], seq_offsets[s+1]) of a packed batch; V_s are its rows with a
+ * non-zero token_mask, n_s = |V_s|, p[t] = softmax(logits[t]) over all E experts:
+ *   counts[s,e] = number of pairs (t, j), t in V_s, with topk_ids[t,j] = e
+ *   loss[s]     = E sum_e f[s,e] P[s,e],  f = counts / (k n_s),  P = sum_{t in V_s} p[t] / n_s
+ * (1 when every expert gets the same share; 0 for a sequence without valid rows).  The caller
+ * weights and sums the sequences' losses.  A row whose logits are all -inf has p = 0.
+ * logits      fp32 [T, E]   (device, read)
+ * topk_ids    int32 [T, k]  (device, read) the routing of moe_route_topk()
+ * seq_offsets int32 [S+1]   (device, read) non-decreasing, within [0, T]; rows outside
+ *             [seq_offsets[0], seq_offsets[S]) belong to no sequence and are not read.
+ *             NULL: one sequence of all T rows (S = 1).
+ * token_mask  uint8 [T]     (device, read) or NULL (every row counts); rows masked out may
+ *             hold any bits
+ * loss fp32 [S], counts int32 [S, E], n_tokens int32 [S] = n_s   (device, written)
+ * ws, ws_bytes              scratch of at least moe_balance_workspace_bytes(T, E, S)
+ * An id outside [0, E) in a valid row, or offsets that decrease or leave [0, T], set
+ * MOE_ERR_DEVICE_INDEX; the results are then undefined.
+ * Supported: k and E as above, 1 <= S < 2^24.  Sums over rows are taken in a fixed order.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+size_t moe_balance_workspace_bytes(int64_t T, int32_t E, int32_t S);
+moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_ids, int64_t T, int32_t E,
+                              int32_t k, const int32_t* seq_offsets, int32_t S,
+                              const uint8_t* token_mask, float* loss, int32_t* counts,
+                              int32_t* n_tokens, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_balance_loss() into the logits (the counts are constants of it), for the
+ * upstream gradient dloss fp32 [S]:
+ *   dlogits[t,e] = g_s p[t,e] (counts[s,e] - sum_j p[t,j] counts[s,j]),
+ *   g_s = dloss[s] E / (k n_s^2),  t in V_s;  0 for every other row.
+ * counts, n_tokens: from moe_balance_loss() on the same rows; logits, seq_offsets,
+ * token_mask as there.  dlogits fp32 [T, E]: every entry written, or with accumulate != 0
+ * added to (rows that count for nothing are then left as they were), e.g. on top of
+ * moe_router_backward()'s.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* counts,
+                                       const int32_t* n_tokens, const float* dloss, int64_t T,
+                                       int32_t E, int32_t k, const int32_t* seq_offsets, int32_t S,
+                                       const uint8_t* token_mask, float* dlogits,
+                                       int32_t accumulate, void* stream);
+
+/* One AdamW step over many tensors (the adapters, or the expert weights in full fine-tuning).
+ * For every element, with t the number of this step, g the gradient times *grad_scale:
+ *   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2,
+ *   w = w (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v / (1 - b2^t)) + eps)
+ * in fp32.  w is the master weight where there is one (the parameter is then its rounding),
+ * else the parameter itself; a bf16 parameter is rounded to nearest.
+ *
+ * States in 32 bits: exp_avg = m and exp_avg_sq = v, fp32 [n].
+ * States in 8 bits: blocks of 256 consecutive elements; exp_avg holds m / s as e4m3 codes,
+ * exp_avg_sq holds sqrt(v) / s as e4m3 codes (one byte each, ceil(n / 256) * 256 bytes), with
+ * one fp32 scale s = (largest |value| of the block) / 448 per block in exp_avg_scale and
+ * exp_avg_sq_scale.  Values are rounded up or down with a probability given by their place
+ * between two codes, from a hash of the element's index and t: rounding to nearest would
+ * never move sqrt(v), which changes by at most 0.05% a step at b2 = 0.999 on a grid 12% wide.
+ * A positive sqrt(v) is never stored as zero.  A block whose largest |value| is below 2^-100
+ * is stored as zeros.  A gradient that is not finite makes its block's scale not finite.  The
+ * step itself uses m and v before they are rounded. */
+typedef struct {
+  void* param;               /* bf16 or fp32, n elements, see the strides */
+  const void* grad;          /* bf16 or fp32 */
+  float* master;             /* fp32 [n] or NULL; only for bf16 parameters */
+  void* exp_avg;             /* [n] fp32, or codes; element order is the view's row-major order */
+  void* exp_avg_sq;
+  float* exp_avg_scale;      /* 8 bits only */
+  float* exp_avg_sq_scale;
+  int64_t size[3];           /* the view's sizes; n = size[0] size[1] size[2] */
+  int64_t param_stride[3];   /* in elements; a contiguous tensor is {1, 1, n} with strides {0, 0, 1} */
+  int64_t grad_stride[3];
+} moe_adamw_tensor_t;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int32_t param_bf16;        /* 1: bf16 parameters, 0: fp32; the same for all tensors of a call */
+  int32_t grad_bf16;
+  int32_t has_master;        /* 1: every tensor has a master weight */
+  int32_t state_bits;        /* 8 or 32 */
+} moe_adamw_config_t;
+
+/* tensors: host array, read before the call returns (a captured call keeps its own copy).
+ * lr (device fp32, or NULL for cfg->lr) and grad_scale (device fp32, or NULL for 1) are read
+ * when the kernels run, so a replayed graph follows them.
+ * step: device int64 [2]; step[0] is the number of steps taken so far, step[1] is zero between
+ * calls.  With advance != 0 the call adds one to step[0] when it is done (several calls that
+ * make up one step: the last one advances).  Calls that share `step` must be ordered.
+ * No two tensors may share parameter or state memory.  Strided views (size[0] or size[1] > 1)
+ * hold fewer than 2^31 elements.
+ * Alignment: exp_avg, exp_avg_sq, master and step 16 bytes, the others their element's.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int32_t n_tensors,
+                            const moe_adamw_config_t* cfg, const float* lr,
+                            const float* grad_scale, int64_t* step, int32_t advance, void* stream);
+
+/* Low-rank adapters of many requests beside a shared projection, in place on its output:
+ *   Y[t] += scale[a] (X[t] A[a]) B[a]     for every row t of request s, a = adapters[s].
+ * Request s is the rows [seq_offsets[s], seq_offsets[s+1]) of a packed batch (a prompt, or one
+ * new token); seq_offsets = NULL means one row per request (S = T).  Rows of requests with
+ * adapters[s] < 0 and rows of no request are left as they were, bit for bit.
+ * X bf16 [T, K] with rows ldx elements apart, Y bf16 [T, N] with rows ldy apart; A bf16
+ * [n_adapters, K, r], B bf16 [n_adapters, r, N] (an adapter of a smaller rank is padded with
+ * zeros), scale fp32 [n_adapters]; seq_offsets int32 [S+1], adapters int32 [S] (device).
+ * X A is summed in fp32; scale X A goes to the second product as the sum of two bf16 (or in
+ * fp32 for short requests); Y is read, added to in fp32 and rounded once.
+ * adapters[s] >= n_adapters, or offsets that decrease or leave [0, T], set
+ * MOE_ERR_DEVICE_INDEX; rows of such requests are left alone or undefined, nothing else.
+ * Supported: K and N multiples of 16, 16 to 2^19; r a multiple of 8, 8 to 128; ldx >= K and
+ * ldy >= N multiples of 8; T, S < 2^24; X and Y 16-byte aligned and not overlapping.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+moe_status_t moe_lora_requests(const moe_bf16_t* X, int64_t ldx, const int32_t* seq_offsets,
+                               const int32_t* adapters, int64_t T, int32_t S, const moe_bf16_t* A,
+                               const moe_bf16_t* B, const float* scale, int32_t n_adapters,
+                               int32_t K, int32_t N, int32_t r, moe_bf16_t* Y, int64_t ldy,
+                               void* stream);
 
 /* Self-test of the failure path (no counterpart on the pages: a check of this
  * library's own error handling).  Every wait of every kernel here is bounded: it

@@ -34,6 +34,8 @@ EXPORTED = (
     "moe_status_string", "moe_profile_enable", "moe_profile_select", "moe_profile_read",
     "moe_permute_noalloc", "moe_router_backward", "moe_grouped_gemm_full_bwd",
     "moe_check_permutation", "moe_selftest_bounded_wait", "moe_route_permute",
+    "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
+    "moe_adamw_step", "moe_lora_requests",
 )
 
 
@@ -47,6 +49,21 @@ class moe_dims_t(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("m", ctypes.c_int32), ("n", ctypes.c_int32),
                 ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("r", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
+
+
+class moe_adamw_tensor_t(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("exp_avg_scale", ctypes.c_void_p), ("exp_avg_sq_scale", ctypes.c_void_p),
+                ("size", ctypes.c_int64 * 3), ("param_stride", ctypes.c_int64 * 3),
+                ("grad_stride", ctypes.c_int64 * 3)]
+
+
+class moe_adamw_config_t(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("param_bf16", ctypes.c_int32), ("grad_bf16", ctypes.c_int32),
+                ("has_master", ctypes.c_int32), ("state_bits", ctypes.c_int32)]
 
 
 _lib_handle = None
@@ -75,6 +92,13 @@ def lib() -> ctypes.CDLL:
         h.moe_unpermute_combine.argtypes = [P, P, P, I64, I32, I32, P, P]
         h.moe_router_backward.argtypes = [P, P, P, P, P, I64, I32, I32, I32, P, P]
         h.moe_selftest_bounded_wait.argtypes = [ctypes.c_uint64, P, P]
+        h.moe_balance_workspace_bytes.argtypes = [I64, I32, I32]
+        h.moe_balance_workspace_bytes.restype = SZ
+        h.moe_balance_loss.argtypes = [P, P, I64, I32, I32, P, I32, P, P, P, P, P, SZ, P]
+        h.moe_balance_loss_backward.argtypes = [P, P, P, P, I64, I32, I32, P, I32, P, P, I32, P]
+        h.moe_adamw_step.argtypes = [ctypes.POINTER(moe_adamw_tensor_t), I32,
+                                     ctypes.POINTER(moe_adamw_config_t), P, P, P, I32, P]
+        h.moe_lora_requests.argtypes = [P, I64, P, P, I64, I32, P, P, P, I32, I32, I32, I32, P, I64, P]
         h.moe_get_device_error.argtypes = [P]
         h.moe_status_string.argtypes = [ctypes.c_int]
         h.moe_status_string.restype = ctypes.c_char_p
@@ -84,7 +108,8 @@ def lib() -> ctypes.CDLL:
         h.moe_profile_read.argtypes = [ctypes.c_int, ctypes.c_char_p, ctypes.c_int,
                                        ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_double)]
         for name in EXPORTED:
-            if name not in ("moe_workspace_bytes", "moe_status_string", "moe_profile_enable"):
+            if name not in ("moe_workspace_bytes", "moe_status_string", "moe_profile_enable",
+                            "moe_balance_workspace_bytes"):
                 getattr(h, name).restype = ctypes.c_int
         _lib_handle = h
     return _lib_handle
@@ -264,6 +289,278 @@ def moe_profile_read() -> dict:
             for i in range(w)}
 
 
+# ---------------------------------------------------------------- balance loss
+def _need(name, t, dtype, shape, device):
+    """A contiguous tensor of this type and shape on this device, or ValueError."""
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _on(t, name, stream):
+    """The stream to launch on for tensors of t's device: `stream`, or that device's current one."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return _stream(stream if stream is not None else torch.cuda.current_stream(t.device))
+
+
+class _Device:
+    """Makes a device current for the launches inside (the library launches on the current one)."""
+
+    def __init__(self, device):
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _check_rows(logits, seq_offsets, token_mask, S):
+    T, E = logits.shape
+    dev = logits.device
+    _need("logits", logits, torch.float32, (T, E), dev)
+    if seq_offsets is not None:
+        _need("seq_offsets", seq_offsets, torch.int32, (S + 1,), dev)
+    elif S != 1:
+        raise ValueError("without seq_offsets there is one sequence")
+    if token_mask is not None:
+        if token_mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("token_mask must be bool or uint8")
+        _need("token_mask", token_mask, token_mask.dtype, (T,), dev)
+    return T, E, dev
+
+
+def moe_balance_workspace_bytes(T: int, E: int, S: int = 1) -> int:
+    return int(lib().moe_balance_workspace_bytes(int(T), int(E), int(S)))
+
+
+def moe_balance_loss(logits, topk_ids, loss, counts, n_tokens, ws, seq_offsets=None, token_mask=None,
+                     stream=None):
+    """Balance loss [S] of the router for every sequence of a packed batch, with the pairs per
+    expert counts [S, E] and the valid rows n_tokens [S] (see include/moelora.h)."""
+    S = loss.shape[0]
+    T, E, dev = _check_rows(logits, seq_offsets, token_mask, S)
+    k = topk_ids.shape[1]
+    _need("topk_ids", topk_ids, torch.int32, (T, k), dev)
+    _need("loss", loss, torch.float32, (S,), dev)
+    _need("counts", counts, torch.int32, (S, E), dev)
+    _need("n_tokens", n_tokens, torch.int32, (S,), dev)
+    if ws.device != dev:
+        raise ValueError(f"the workspace must be on {dev}")
+    st = _on(logits, "logits", stream)
+    with _Device(dev):
+        _check("moe_balance_loss", lib().moe_balance_loss(
+            _ptr(logits), _ptr(topk_ids), T, E, k, _ptr(seq_offsets), S, _ptr(token_mask), _ptr(loss),
+            _ptr(counts), _ptr(n_tokens), _ptr(ws), ws.numel() * ws.element_size(), st))
+
+
+def moe_balance_loss_backward(logits, counts, n_tokens, dloss, k, dlogits, seq_offsets=None,
+                              token_mask=None, accumulate=False, stream=None):
+    """Gradient of moe_balance_loss into the logits for the upstream gradient dloss [S], written
+    to dlogits [T, E] or added to it."""
+    S = dloss.shape[0]
+    T, E, dev = _check_rows(logits, seq_offsets, token_mask, S)
+    _need("counts", counts, torch.int32, (S, E), dev)
+    _need("n_tokens", n_tokens, torch.int32, (S,), dev)
+    _need("dloss", dloss, torch.float32, (S,), dev)
+    _need("dlogits", dlogits, torch.float32, (T, E), dev)
+    st = _on(logits, "logits", stream)
+    with _Device(dev):
+        _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
+            _ptr(logits), _ptr(counts), _ptr(n_tokens), _ptr(dloss), T, E, int(k), _ptr(seq_offsets), S,
+            _ptr(token_mask), _ptr(dlogits), 1 if accumulate else 0, st))
+
+
+# ---------------------------------------------------------------- adapters of many requests
+def moe_lora_requests(X, adapters, A, B, scale, Y, seq_offsets=None, stream=None):
+    """Y[t] += scale[a] (X[t] A[a]) B[a] in place, a = adapters[request of row t] (negative: row
+    left alone).  X [T, K] and Y [T, N] may be views with a row stride; seq_offsets [S + 1] gives
+    the requests' rows, None one row per request (see include/moelora.h)."""
+    T, K = X.shape
+    n, _, r = A.shape
+    N = Y.shape[1]
+    dev = X.device
+    S = adapters.shape[0]
+    for name, t, w in (("X", X, K), ("Y", Y, N)):
+        if (t.dtype != torch.bfloat16 or t.shape[0] != T or t.device != dev or (w > 1 and t.stride(1) != 1)):
+            raise ValueError(f"{name} must be bfloat16 [{T}, {w}] on {dev} with unit stride inside its rows")
+    _need("A", A, torch.bfloat16, (n, K, r), dev)
+    _need("B", B, torch.bfloat16, (n, r, N), dev)
+    _need("scale", scale, torch.float32, (n,), dev)
+    _need("adapters", adapters, torch.int32, (S,), dev)
+    if seq_offsets is not None:
+        _need("seq_offsets", seq_offsets, torch.int32, (S + 1,), dev)
+    elif S != T:
+        raise ValueError("without seq_offsets every row is a request: adapters must have one entry per row")
+    st = _on(X, "X", stream)
+    # (the stride of a single row means nothing)
+    ldx, ldy = (X.stride(0), Y.stride(0)) if T > 1 else (K, N)
+    with _Device(dev):
+        _check("moe_lora_requests", lib().moe_lora_requests(
+            _ptr(X), ldx, _ptr(seq_offsets), _ptr(adapters), T, S, _ptr(A), _ptr(B), _ptr(scale), n, K, N, r,
+            _ptr(Y), ldy, st))
+
+
+# ---------------------------------------------------------------- AdamW
+STATE_BLOCK = 256     # elements that share a scale in 8-bit states
+
+
+def _joint_view(p, g):
+    """Sizes and the two tensors' strides of a common view of at most three dimensions."""
+    dims = [(n, sp, sg) for n, sp, sg in zip(p.shape, p.stride(), g.stride()) if n != 1]
+    out = []
+    for n, sp, sg in dims:
+        if out and out[-1][1] == sp * n and out[-1][2] == sg * n:
+            out[-1] = (out[-1][0] * n, sp, sg)
+        else:
+            out.append((n, sp, sg))
+    if not out:
+        out = [(1, 1, 1)]
+    if len(out) > 3:
+        raise ValueError(f"a tensor of shape {tuple(p.shape)} with strides {p.stride()} (gradient {g.stride()}) "
+                         "does not fit a view of three dimensions")
+    return [(1, 0, 0)] * (3 - len(out)) + out
+
+
+class AdamW:
+    """AdamW over many tensors in one launch (moe_adamw_step), e.g. the adapters of all layers.
+
+    params: bf16 or fp32 tensors, updated in place; grads: a gradient buffer for each (bf16 or
+    fp32, the same shape), kept and read at every step().  Both may be strided views of up to
+    three dimensions (SplitGateUpAdapters' views).  state_bits: 32 (fp32 moments) or 8 (e4m3
+    codes of m and of sqrt(v) with an fp32 scale per 256 elements).  master_weights: an fp32
+    copy of every bf16 parameter that the step updates and the parameter is rounded from; without
+    it a change smaller than half a bf16 step of the weight is lost.
+
+    lr may be set between steps, or be a device fp32 tensor that captured steps read.  The
+    states live in flat tensors, each parameter's part beginning at a multiple of 256 elements
+    (`starts`): exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale (8 bits), master.  steps is
+    the number of steps taken, a device int64 that step() moves on, so that a captured step
+    counts too.  Steps of one optimizer must be ordered on the device."""
+
+    def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                 state_bits: int = 32, master_weights: bool = False):
+        self.params, self.grads = list(params), list(grads)
+        if len(self.params) != len(self.grads) or not self.params:
+            raise ValueError("AdamW needs one gradient buffer for each of one or more parameters")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        self.device = dev = self.params[0].device
+        if dev.type != "cuda":
+            raise ValueError("parameters must be on a CUDA device")
+        self.lr, self.state_bits = lr, state_bits
+        ok = (torch.bfloat16, torch.float32)
+        groups, taken, at = {}, set(), 0
+        self.starts, views = [], []
+        for i, (p, g) in enumerate(zip(self.params, self.grads)):
+            if p.dtype not in ok or g.dtype not in ok or p.shape != g.shape or p.device != dev or g.device != dev:
+                raise ValueError(f"parameter {i}: bf16 or fp32 with a gradient of its shape on {dev} is needed")
+            view = _joint_view(p, g)
+            if any(n > 1 and sp == 0 for n, sp, _ in view):
+                raise ValueError(f"parameter {i} has several elements in one place")
+            if p.numel() and p.data_ptr() in taken:
+                raise ValueError(f"parameter {i} begins where another one does")
+            taken.add(p.data_ptr())
+            if any(v[0] > 1 for v in view[:2]) and p.numel() >= 1 << 31:
+                raise ValueError(f"parameter {i}: a strided view holds fewer than 2^31 elements")
+            views.append(view)
+            self.starts.append(at)
+            at += -(-p.numel() // STATE_BLOCK) * STATE_BLOCK
+            with_master = master_weights and p.dtype == torch.bfloat16
+            groups.setdefault((p.dtype == torch.bfloat16, g.dtype == torch.bfloat16, with_master), []).append(i)
+        if state_bits == 8:
+            self.exp_avg = torch.zeros(at, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+            self.exp_avg_sq = torch.zeros(at, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+            self.exp_avg_scale = torch.zeros(at // STATE_BLOCK, dtype=torch.float32, device=dev)
+            self.exp_avg_sq_scale = torch.zeros(at // STATE_BLOCK, dtype=torch.float32, device=dev)
+        else:
+            self.exp_avg = torch.zeros(at, dtype=torch.float32, device=dev)
+            self.exp_avg_sq = torch.zeros(at, dtype=torch.float32, device=dev)
+            self.exp_avg_scale = self.exp_avg_sq_scale = None
+        self.master = None
+        if any(g[2] for g in groups):
+            self.master = torch.zeros(at, dtype=torch.float32, device=dev)
+            for i in (i for g, idx in groups.items() if g[2] for i in idx):
+                self._part(self.master, i).copy_(self.params[i])
+        self._count = torch.zeros(2, dtype=torch.int64, device=dev)
+        self.steps = self._count[0]
+        elem = 1 if state_bits == 8 else 4
+        self._calls = []
+        for (p16, g16, master), idx in groups.items():
+            table = (moe_adamw_tensor_t * len(idx))()
+            for row, i in zip(table, idx):
+                row.param, row.grad = self.params[i].data_ptr(), self.grads[i].data_ptr()
+                row.exp_avg = self.exp_avg.data_ptr() + self.starts[i] * elem
+                row.exp_avg_sq = self.exp_avg_sq.data_ptr() + self.starts[i] * elem
+                if state_bits == 8:
+                    row.exp_avg_scale = self.exp_avg_scale.data_ptr() + self.starts[i] // STATE_BLOCK * 4
+                    row.exp_avg_sq_scale = self.exp_avg_sq_scale.data_ptr() + self.starts[i] // STATE_BLOCK * 4
+                if master:
+                    row.master = self.master.data_ptr() + self.starts[i] * 4
+                for d, (n, sp, sg) in enumerate(views[i]):
+                    row.size[d], row.param_stride[d], row.grad_stride[d] = n, sp, sg
+            cfg = moe_adamw_config_t(0.0, betas[0], betas[1], eps, weight_decay, int(p16), int(g16), int(master),
+                                     state_bits)
+            self._calls.append((table, len(idx), cfg, ctypes.byref(cfg)))
+
+    def _part(self, flat, i):
+        p = self.params[i]
+        return flat[self.starts[i]:self.starts[i] + p.numel()].view(p.shape)
+
+    def step(self, grad_scale=None, stream=None):
+        """One step with the gradients in the buffers, times grad_scale (a device fp32 tensor of
+        one element) where given."""
+        lr_dev = None
+        if isinstance(self.lr, torch.Tensor):
+            lr_dev = self.lr
+            _need("lr", lr_dev, torch.float32, tuple(lr_dev.shape) if lr_dev.numel() == 1 else (1,), self.device)
+        if grad_scale is not None:
+            _need("grad_scale", grad_scale, torch.float32,
+                  tuple(grad_scale.shape) if grad_scale.numel() == 1 else (1,), self.device)
+        st = _on(self._count, "parameters", stream)
+        last = len(self._calls) - 1
+        fn, count = lib().moe_adamw_step, _ptr(self._count)
+        with _Device(self.device):
+            for j, (table, n, cfg, ref) in enumerate(self._calls):
+                if lr_dev is None:
+                    cfg.lr = self.lr
+                _check("moe_adamw_step", fn(table, n, ref, _ptr(lr_dev), _ptr(grad_scale), count, int(j == last), st))
+
+    def moments(self, i: int):
+        """(m, v) of parameter i as fp32 tensors of its shape (what the codes stand for in 8 bits)."""
+        if self.state_bits == 32:
+            return self._part(self.exp_avg, i), self._part(self.exp_avg_sq, i)
+        a = self.starts[i]
+        n = -(-self.params[i].numel() // STATE_BLOCK) * STATE_BLOCK
+        out = []
+        for codes, scales in ((self.exp_avg, self.exp_avg_scale), (self.exp_avg_sq, self.exp_avg_sq_scale)):
+            x = codes[a:a + n].float().view(-1, STATE_BLOCK)
+            x = x * scales[a // STATE_BLOCK:(a + n) // STATE_BLOCK, None]
+            out.append(x.view(-1)[:self.params[i].numel()].view(self.params[i].shape))
+        return out[0], out[1].square()
+
+    _STATE = ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "master", "steps")
+
+    def state_dict(self) -> dict:
+        """The optimizer's own tensors (not copies), for checkpoints; None where it has none."""
+        return {k: getattr(self, k) for k in self._STATE}
+
+    def load_state_dict(self, state: dict):
+        """Copies a state_dict() of an optimizer over the same parameters and settings."""
+        for k in self._STATE:
+            mine, other = getattr(self, k), state[k]
+            if (mine is None) != (other is None) or (mine is not None and (mine.shape != other.shape
+                                                                          or mine.dtype != other.dtype)):
+                raise ValueError(f"{k} does not fit this optimizer")
+        for k in self._STATE:
+            if getattr(self, k) is not None:
+                getattr(self, k).copy_(state[k])
+
+
 # ---------------------------------------------------------------- whole layer
 @dataclass
 class LayerBuffers:
@@ -365,6 +662,54 @@ def layer_step(inp: dict, k: int, scale: float, buf: LayerBuffers, stream=None):
     """One pass of the whole hot path: forward then backward against inp['dY']."""
     layer_forward(inp, k, scale, buf, stream)
     layer_backward(inp, inp["dY"], k, scale, buf, stream)
+    return buf
+
+
+@dataclass
+class BalanceBuffers:
+    """Device buffers of the balance loss in a training step: the loss and its upstream gradient
+    per sequence, the counts, and the gradient into the router logits."""
+    loss: torch.Tensor
+    dloss: torch.Tensor
+    counts: torch.Tensor
+    n_tokens: torch.Tensor
+    dlogits: torch.Tensor
+    ws: torch.Tensor
+
+
+def alloc_balance(T, E, S=1, weight=0.01, device="cuda") -> BalanceBuffers:
+    """Buffers for S sequences; every sequence's loss gets the weight `weight` / S."""
+    f32 = dict(dtype=torch.float32, device=device)
+    i32 = dict(dtype=torch.int32, device=device)
+    wsb = moe_balance_workspace_bytes(T, E, S)
+    if wsb == 0:
+        raise MoEError("moe_balance_workspace_bytes", MOE_ERR_UNSUPPORTED, "unsupported shape")
+    return BalanceBuffers(loss=torch.empty(S, **f32), dloss=torch.full((S,), weight / S, **f32),
+                          counts=torch.empty(S, E, **i32), n_tokens=torch.empty(S, **i32),
+                          dlogits=torch.empty(T, E, **f32),
+                          ws=torch.empty(wsb, dtype=torch.uint8, device=device))
+
+
+def layer_train_step(inp: dict, k: int, scale: float, buf: LayerBuffers, opt: AdamW,
+                     balance: BalanceBuffers | None = None, seq_offsets=None, token_mask=None, group=None,
+                     grad_scale=None, stream=None):
+    """One training step of the layer: forward, backward against inp['dY'], the adapter gradients
+    summed over the data-parallel ranks, and the optimizer's step (opt holds the layer's adapters
+    and buf's gradient buffers).  With `balance` the router's gradient comes too: balance.dlogits
+    is that of the output through the routing weights plus that of the balance loss."""
+    layer_forward(inp, k, scale, buf, stream)
+    if balance is not None:
+        moe_balance_loss(inp["logits"], buf.ids, balance.loss, balance.counts, balance.n_tokens, balance.ws,
+                         seq_offsets, token_mask, stream)
+        moe_router_backward(inp["dY"], buf.Y_sorted, buf.ids, buf.w, buf.pair_pos, inp["logits"].shape[1],
+                            balance.dlogits, stream)
+        moe_balance_loss_backward(inp["logits"], balance.counts, balance.n_tokens, balance.dloss, k,
+                                  balance.dlogits, seq_offsets, token_mask, True, stream)
+    layer_backward(inp, inp["dY"], k, scale, buf, stream)
+    from .dp import allreduce_adapter_grads
+    with torch.cuda.stream(stream):       # (None: the current stream stays)
+        allreduce_adapter_grads([buf.dA_gu, buf.dB_gu, buf.dA_d, buf.dB_d], group)
+    opt.step(grad_scale, stream)
     return buf
 
 

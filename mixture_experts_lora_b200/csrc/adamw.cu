@@ -1,0 +1,305 @@
+// One AdamW step over many tensors in one launch, states in fp32 or in 8 bits.
+//
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
+//   w = w (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// Every element is read and written once: the step is bound by HBM.  The tensors' table
+// travels in the kernel's parameters, so a call needs no copy to the device and a captured
+// call keeps its own table.  Each tensor is cut into chunks of 2048 elements, one block
+// each; a warp owns 256 consecutive elements, which is also the block of elements that
+// shares a scale in 8 bits, so its maximum is a warp reduction.
+//
+// 8 bits: e4m3 codes of m and of sqrt(v) (the root halves the exponent range that a block
+// has to span), scaled so that the block's largest value is 448.  A code is the value with
+// 3 mantissa bits; the bits below are rounded up with probability equal to their value
+// (random bits: a 32-bit integer mix of the element's index and t), so that the averages
+// move as they should although one step changes them by less than a code.
+#include <cuda_fp8.h>
+
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlockElems = 256;     // elements that share a scale, and a warp's share
+constexpr int kChunk = (kThreads / 32) * kBlockElems;
+
+struct Tensor {
+  void* p;
+  const void* g;
+  float* w;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  int64_t n;
+  uint32_t d1, d2;         // strided views: sizes of the two inner dimensions; d2 = 0: contiguous
+  int64_t ps[3], gs[3];
+};
+
+template <int NT>
+struct AdamwArgs {
+  Tensor t[NT];
+  int32_t chunk0[NT + 1];  // first chunk of each tensor
+  int n;
+  float lr, b1, b2, eps, wd, one_b1, one_b2, ln_b1, ln_b2;
+  const float* lr_dev;
+  const float* grad_scale;
+  long long* step;
+  int advance;
+};
+
+__device__ __forceinline__ uint32_t mix32(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x9E3779B9u;
+  x = (x ^ (x >> 15)) * 0xBB67AE85u;
+  return x ^ (x >> 16);
+}
+
+// Largest |value| of the warp's elements; a NaN among them wins.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// e4m3 code of x (x >= 0), |x| inv <= 448: moving e4m3's exponents to the bottom of fp32's
+// (times 2^-120) makes e4m3's subnormals fp32's own, after which 20 mantissa bits go.
+__device__ __forceinline__ uint32_t encode_abs(float x, float inv, uint32_t rnd16) {
+  const uint32_t bits = __float_as_uint(__fmul_rn(__fmul_rn(x, inv), 0x1p-120f));
+  const uint32_t c = (bits + (rnd16 << 4)) >> 20;
+  return c < 0x7Eu ? c : 0x7Eu;
+}
+
+__device__ __forceinline__ float decode(uint8_t c) {
+  __nv_fp8_e4m3 q;
+  q.__x = c;
+  return static_cast<float>(q);
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_as_float(const void* p, int64_t i) {
+  if constexpr (BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  else return static_cast<const float*>(p)[i];
+}
+template <bool BF16>
+__device__ __forceinline__ void store_float(void* p, int64_t i, float v) {
+  if constexpr (BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<float*>(p)[i] = v;
+}
+
+// Offset of element i (row-major index of the view) under strides st.
+__device__ __forceinline__ int64_t view_offset(const Tensor& t, int64_t i, const int64_t (&st)[3]) {
+  if (t.d2 == 0) return i;
+  const uint32_t u = (uint32_t)i, r = u / t.d2, c = u - r * t.d2, a = r / t.d1, b = r - a * t.d1;
+  return a * st[0] + b * st[1] + c * st[2];
+}
+
+template <int NT, bool PBF16, bool GBF16, bool MASTER, bool BITS8>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwArgs<NT> a) {
+  pdl_begin();
+  const int lane = lane_id();
+  const long long t_step = a.step[0] + 1;
+  const float lr = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
+  const float gscale = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
+  // 1 - b^t = -expm1(t ln b): relative accuracy even where b^t is near 1
+  const float tf = (float)t_step;
+  const float c1 = lr / -expm1f(tf * a.ln_b1);
+  const float rbc2 = 1.0f / sqrtf(-expm1f(tf * a.ln_b2));
+  const float keep = 1.0f - lr * a.wd;
+  const uint32_t seed = mix32((uint32_t)t_step);
+  const int n_chunks = a.chunk0[a.n];
+  for (int c = blockIdx.x; c < n_chunks; c += gridDim.x) {
+    int lo = 0, hi = a.n;                      // the chunk's tensor: chunk0[lo] <= c < chunk0[lo + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.chunk0[mid] <= c) lo = mid; else hi = mid;
+    }
+    const Tensor& t = a.t[lo];
+    const int64_t base = (int64_t)(c - a.chunk0[lo]) * kChunk + warp_id() * kBlockElems;
+    if (base >= t.n) continue;
+    const int64_t blk = base / kBlockElems;
+    float msc = 0.f, vsc = 0.f;
+    if constexpr (BITS8) { msc = t.ms[blk]; vsc = t.vs[blk]; }
+    float m[8], u[8];
+    float mtop = 0.f, vtop = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t i = base + 32 * j + lane;
+      m[j] = u[j] = 0.f;
+      if (i >= t.n) continue;
+      const int64_t po = view_offset(t, i, t.ps);
+      const float g = load_as_float<GBF16>(t.g, view_offset(t, i, t.gs)) * gscale;
+      float mi, vi;
+      if constexpr (BITS8) {
+        mi = decode(static_cast<const uint8_t*>(t.m)[i]) * msc;
+        vi = decode(static_cast<const uint8_t*>(t.v)[i]) * vsc;
+        vi *= vi;
+      } else {
+        mi = static_cast<const float*>(t.m)[i];
+        vi = static_cast<const float*>(t.v)[i];
+      }
+      mi = a.b1 * mi + a.one_b1 * g;
+      vi = a.b2 * vi + a.one_b2 * (g * g);
+      const float root = sqrtf(vi);
+      float w = MASTER ? t.w[i] : load_as_float<PBF16>(t.p, po);
+      w = w * keep - c1 * (mi / (root * rbc2 + a.eps));
+      if constexpr (MASTER) t.w[i] = w;
+      store_float<PBF16>(t.p, po, w);
+      if constexpr (BITS8) {
+        m[j] = mi;
+        u[j] = root;
+        mtop = max_nan(mtop, fabsf(mi));
+        vtop = max_nan(vtop, root);
+      } else {
+        static_cast<float*>(t.m)[i] = mi;
+        static_cast<float*>(t.v)[i] = vi;
+      }
+    }
+    if constexpr (BITS8) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        mtop = max_nan(mtop, __shfl_xor_sync(0xffffffffu, mtop, o));
+        vtop = max_nan(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
+      }
+      if (mtop < 0x1p-100f) mtop = 0.f;
+      if (vtop < 0x1p-100f) vtop = 0.f;
+      const float minv = mtop == 0.f ? 0.f : 448.0f / mtop, vinv = vtop == 0.f ? 0.f : 448.0f / vtop;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t i = base + 32 * j + lane;
+        const uint32_t h = mix32((uint32_t)i ^ seed);
+        uint32_t cm = encode_abs(fabsf(m[j]), minv, h & 0xffffu);
+        if (m[j] < 0.f && cm != 0) cm |= 0x80u;
+        uint32_t cv = encode_abs(u[j], vinv, h >> 16);
+        if (u[j] > 0.f && vinv != 0.f && cv == 0) cv = 1u;
+        // (the codes' memory is whole blocks)
+        static_cast<uint8_t*>(t.m)[i] = (uint8_t)cm;
+        static_cast<uint8_t*>(t.v)[i] = (uint8_t)cv;
+      }
+      if (lane == 0) {
+        t.ms[blk] = mtop / 448.0f;
+        t.vs[blk] = vtop / 448.0f;
+      }
+    }
+  }
+  if (a.advance) {
+    // every block has read the step before it arrives; the last one moves it on
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      unsigned long long* arrived = reinterpret_cast<unsigned long long*>(a.step + 1);
+      if (atomicAdd(arrived, 1ull) == gridDim.x - 1) {
+        a.step[1] = 0;
+        a.step[0] = t_step;
+      }
+    }
+  }
+}
+
+template <int NT, bool P, bool G, bool M, bool B8>
+cudaError_t launch(const moe_adamw_tensor_t* src, int n, const moe_adamw_config_t& c, const float* lr,
+                   const float* gscale, int64_t* step, bool advance, cudaStream_t s) {
+  AdamwArgs<NT> a;
+  int64_t chunks = 0;
+  for (int i = 0; i < n; ++i) {
+    const moe_adamw_tensor_t& t = src[i];
+    Tensor& d = a.t[i];
+    d.p = t.param; d.g = t.grad; d.w = t.master; d.m = t.exp_avg; d.v = t.exp_avg_sq;
+    d.ms = t.exp_avg_scale; d.vs = t.exp_avg_sq_scale;
+    d.n = t.size[0] * t.size[1] * t.size[2];
+    const bool flat = t.size[0] == 1 && t.size[1] == 1 && t.param_stride[2] == 1 && t.grad_stride[2] == 1;
+    d.d1 = (uint32_t)t.size[1];
+    d.d2 = flat ? 0u : (uint32_t)t.size[2];
+    for (int k = 0; k < 3; ++k) { d.ps[k] = t.param_stride[k]; d.gs[k] = t.grad_stride[k]; }
+    a.chunk0[i] = (int32_t)chunks;
+    chunks += (d.n + kChunk - 1) / kChunk;
+  }
+  if (chunks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  a.chunk0[n] = (int32_t)chunks;
+  a.n = n;
+  a.lr = (float)c.lr; a.b1 = (float)c.beta1; a.b2 = (float)c.beta2; a.eps = (float)c.eps;
+  a.wd = (float)c.weight_decay;
+  a.one_b1 = (float)(1.0 - c.beta1); a.one_b2 = (float)(1.0 - c.beta2);
+  a.ln_b1 = (float)std::log(c.beta1); a.ln_b2 = (float)std::log(c.beta2);
+  a.lr_dev = lr; a.grad_scale = gscale;
+  a.step = reinterpret_cast<long long*>(step);
+  a.advance = advance ? 1 : 0;
+  const int64_t cap = (int64_t)device_sms() * 64;
+  const unsigned grid = (unsigned)(chunks < 1 ? 1 : chunks < cap ? chunks : cap);
+  ProfScope ps(K_ADAMW, s);
+  return launch_pdl(adamw_kernel<NT, P, G, M, B8>, dim3(grid), dim3(kThreads), 0, s, 1, a);
+}
+
+// Tensors per launch: a short table for few (kernel parameters are copied at every launch),
+// a long one that fills the 32764 bytes that a kernel's parameters may take.
+constexpr int kShort = 16, kLong = 256;
+static_assert(sizeof(AdamwArgs<kLong>) <= 32764, "kernel parameters");
+
+template <bool P, bool G, bool M, bool B8>
+cudaError_t launch_all(const moe_adamw_tensor_t* src, int n, const moe_adamw_config_t& c, const float* lr,
+                       const float* gscale, int64_t* step, bool advance, cudaStream_t s) {
+  for (int i = 0; i == 0 || i < n; i += kLong) {
+    const int k = n - i < kLong ? n - i : kLong;
+    const bool last = advance && i + kLong >= n;
+    const cudaError_t e = k <= kShort ? launch<kShort, P, G, M, B8>(src + i, k, c, lr, gscale, step, last, s)
+                                      : launch<kLong, P, G, M, B8>(src + i, k, c, lr, gscale, step, last, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaGetLastError();
+}
+
+bool aligned_to(const void* p, size_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int32_t n_tensors,
+                                       const moe_adamw_config_t* cfg, const float* lr,
+                                       const float* grad_scale, int64_t* step, int32_t advance,
+                                       void* stream) {
+  NvtxRange nr("moe_adamw_step");
+  if (cfg == nullptr || n_tensors < 0 || (n_tensors > 0 && tensors == nullptr)) return MOE_ERR_INVALID_ARG;
+  const moe_adamw_config_t& c = *cfg;
+  if (!std::isfinite(c.lr) || !std::isfinite(c.weight_decay) || !(c.eps >= 0) || !std::isfinite(c.eps) ||
+      !(c.beta1 >= 0 && c.beta1 < 1) || !(c.beta2 >= 0 && c.beta2 < 1))
+    return MOE_ERR_INVALID_ARG;
+  if (c.state_bits != 8 && c.state_bits != 32) return MOE_ERR_UNSUPPORTED;
+  const bool p16 = c.param_bf16 != 0, g16 = c.grad_bf16 != 0, master = c.has_master != 0, b8 = c.state_bits == 8;
+  if (master && !p16) return MOE_ERR_UNSUPPORTED;
+  if (!aligned16(step)) return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < n_tensors; ++i) {
+    const moe_adamw_tensor_t& t = tensors[i];
+    int64_t n = 1;
+    for (int k = 0; k < 3; ++k) {
+      if (t.size[k] < 0 || t.param_stride[k] < 0 || t.grad_stride[k] < 0) return MOE_ERR_INVALID_ARG;
+      if (t.size[k] > (int64_t(1) << 40) || n > (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
+      n *= t.size[k];
+      // two elements of one parameter in one place would race
+      if (t.size[k] > 1 && t.param_stride[k] == 0) return MOE_ERR_INVALID_ARG;
+    }
+    if (n == 0) continue;
+    if (n > (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
+    const bool flat = t.size[0] == 1 && t.size[1] == 1 && t.param_stride[2] == 1 && t.grad_stride[2] == 1;
+    if (!flat && n >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    if (!aligned_to(t.param, p16 ? 2 : 4) || !aligned_to(t.grad, g16 ? 2 : 4)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(t.exp_avg) || !aligned16(t.exp_avg_sq)) return MOE_ERR_INVALID_ARG;
+    if (b8 && (!aligned_to(t.exp_avg_scale, 4) || !aligned_to(t.exp_avg_sq_scale, 4))) return MOE_ERR_INVALID_ARG;
+    if (master && !aligned16(t.master)) return MOE_ERR_INVALID_ARG;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool adv = advance != 0;
+#define MOE_ADAMW(P, G, M) \
+  (b8 ? launch_all<P, G, M, true>(tensors, n_tensors, c, lr, grad_scale, step, adv, s) \
+      : launch_all<P, G, M, false>(tensors, n_tensors, c, lr, grad_scale, step, adv, s))
+  cudaError_t e;
+  if (p16 && master) e = g16 ? MOE_ADAMW(true, true, true) : MOE_ADAMW(true, false, true);
+  else if (p16) e = g16 ? MOE_ADAMW(true, true, false) : MOE_ADAMW(true, false, false);
+  else e = g16 ? MOE_ADAMW(false, true, false) : MOE_ADAMW(false, false, false);
+#undef MOE_ADAMW
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

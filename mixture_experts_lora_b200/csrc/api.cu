@@ -10,8 +10,6 @@
 #include "common.cuh"
 #include "internal.h"
 
-#include <nvtx3/nvToolsExt.h>
-
 namespace moe {
 
 // Device status word (one per device); kernels set it with atomicCAS, the host
@@ -43,18 +41,6 @@ int* status_ptr() {
   return ptrs[dev];
 }
 
-int device_sms() {
-  static int sms[kMaxDevices] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
-  if (sms[dev] == 0) {
-    int v = 0;
-    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-    sms[dev] = v > 0 ? v : 148;
-  }
-  return sms[dev];
-}
-
 inline int rank_padded(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
 // Row chunk of the adapter-gradient kernel.  An expert cut into several chunks
@@ -79,8 +65,6 @@ inline int64_t chunk_rows_for(const moe_dims_t& d, int64_t P) {
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 moe_status_t check_dims(const moe_dims_t* d) {
   if (d == nullptr) return MOE_ERR_INVALID_ARG;
@@ -318,18 +302,21 @@ void* current_context() {
 
 int* moe_status_word() { return status_ptr(); }
 
+int device_sms() {
+  static int sms[kMaxDevices] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
+  if (sms[dev] == 0) {
+    int v = 0;
+    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+    sms[dev] = v > 0 ? v : 148;
+  }
+  return sms[dev];
+}
+
 }  // namespace moe
 
 using namespace moe;
-
-namespace {
-// An NVTX range named after the entry point around each call (visible to profilers
-// that record NVTX; a no-op otherwise).
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-};
-}  // namespace
 
 extern "C" {
 
@@ -345,7 +332,7 @@ const char* moe_status_string(moe_status_t s) {
     case MOE_ERR_UNSUPPORTED: return "unsupported shape";
     case MOE_ERR_WORKSPACE: return "workspace too small";
     case MOE_ERR_CUDA: return "CUDA error";
-    case MOE_ERR_DEVICE_INDEX: return "expert id out of range (device)";
+    case MOE_ERR_DEVICE_INDEX: return "expert id, adapter id or sequence offset out of range (device)";
     case MOE_ERR_TIMEOUT: return "bounded wait expired (device)";
     case MOE_ERR_DEVICE_CHECK: return "permutation invariant broken (device check)";
   }

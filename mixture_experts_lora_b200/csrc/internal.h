@@ -7,7 +7,20 @@
 
 #include "../../include/moelora.h"
 
+#include <nvtx3/nvToolsExt.h>
+
 namespace moe {
+
+// An NVTX range named after the entry point around each call (visible to profilers
+// that record NVTX; a no-op otherwise).
+struct NvtxRange {
+  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
+  ~NvtxRange() { nvtxRangePop(); }
+};
+
+inline bool aligned16(const void* p) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
 
 struct TileInfo;
 struct TableBuild;
@@ -44,7 +57,8 @@ enum KernelKind : int {
   K_ROUTE = 0, K_PERM_HIST, K_PERM_SCATTER,
   K_GEMM_GATEUP_FWD, K_GEMM_DOWN_FWD, K_GEMM_DOWN_BWD, K_GEMM_GATEUP_BWD, K_WGRAD,
   K_COMBINE, K_MEMSET, K_RANK_XA, K_RANK_HA, K_RANK_T1, K_RANK_T2,
-  K_ROUTER_BWD, K_GEMM_DW_GU, K_GEMM_DW_D, K_NUM_KINDS
+  K_ROUTER_BWD, K_GEMM_DW_GU, K_GEMM_DW_D, K_BALANCE, K_BALANCE_SUM, K_BALANCE_BWD, K_ADAMW,
+  K_LORA_REQUESTS, K_NUM_KINDS
 };
 extern const char* const kKernelNames[K_NUM_KINDS];
 bool prof_enabled();
@@ -61,6 +75,8 @@ struct ProfScope {
 
 // Device address of the status word of the current device (api.cu), or nullptr.
 int* moe_status_word();
+// Streaming multiprocessors of the current device.
+int device_sms();
 // The current CUDA context (a CUcontext), or nullptr: caches of device addresses key
 // on it, so that a device reset or a new primary context looks them up again.
 void* current_context();

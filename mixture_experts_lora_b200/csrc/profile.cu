@@ -19,7 +19,8 @@ const char* const kKernelNames[K_NUM_KINDS] = {
     "gemm_gateup_fwd",   "gemm_down_fwd",     "gemm_down_bwd",
     "gemm_gateup_bwd",   "lora_wgrad",        "unpermute_combine", "memset",
     "rank_xa",           "rank_ha",           "rank_t1",          "rank_t2",
-    "router_backward",   "gemm_dw_gu",        "gemm_dw_d"};
+    "router_backward",   "gemm_dw_gu",        "gemm_dw_d",         "balance_loss",
+    "balance_sum",       "balance_backward",  "adamw",            "lora_requests"};
 
 namespace {
 struct Rec {

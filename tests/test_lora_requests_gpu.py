@@ -1,0 +1,205 @@
+"""The adapters of many requests against the fp64 definition.
+
+Bound of an entry: half a bf16 step of the result (2^-8); X A and its product with B in fp32
+with chains of at most K / 8 + 300 additions, u = 2^-24 each, of the products' absolute values;
+X A as the sum of two bf16, 2^-17 of itself.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_lora_b200 as ml
+import oracle.train_serve_oracle as O
+
+from gpu_common import ensure_built
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_built()
+
+
+class Case:
+    def __init__(self, T, K, N, r, n, adapters, off=None, seed=0, ldx=0, ldy=0):
+        g = torch.Generator().manual_seed(seed)
+        self.Xs = torch.randn(T, K + ldx, generator=g).to(BF).cuda()
+        self.Ys = torch.randn(T, N + ldy, generator=g).to(BF).cuda()
+        self.X, self.Y = self.Xs[:, ldx:], self.Ys[:, ldy:]
+        self.A = (torch.randn(n, K, r, generator=g) / K ** 0.5).to(BF).cuda()
+        self.B = torch.randn(n, r, N, generator=g).to(BF).cuda()
+        self.scale = (torch.rand(n, generator=g) + 0.5).cuda()
+        self.adapters, self.off, self.ldy = adapters, off, ldy
+        self.ad = torch.tensor(adapters, dtype=torch.int32, device="cuda")
+        self.offs = None if off is None else torch.tensor(off, dtype=torch.int32, device="cuda")
+
+    def call(self, stream=None):
+        ml.moe_lora_requests(self.X, self.ad, self.A, self.B, self.scale, self.Y, self.offs, stream)
+
+    def run(self):
+        self.before = self.Ys.clone()
+        self.call()
+        torch.cuda.synchronize()
+        assert ml.moe_get_device_error() == ml.MOE_OK
+        return self
+
+    def check(self):
+        f = lambda t: t.double().cpu().numpy()      # noqa: E731
+        X, A, B, c, Y0 = f(self.X), f(self.A), f(self.B), f(self.scale), f(self.before[:, self.ldy:])
+        ref = O.lora_requests(X, self.adapters, A, B, c, Y0, self.off)
+        zero = np.zeros_like(Y0)
+        both = O.lora_requests(np.abs(X), self.adapters, np.abs(A), np.abs(B), c, zero, self.off)
+        K = X.shape[1]
+        tol = 2.0 ** -8 * np.abs(ref) + ((K / 8 + 300) * U + 2.0 ** -17) * both
+        assert np.all(np.abs(f(self.Y) - ref) <= tol)
+        # rows without an adapter, rows of no request and the other columns: bit for bit
+        idle = torch.ones(X.shape[0], dtype=torch.bool)
+        for s, a in enumerate(self.adapters):
+            lo, hi = (s, s + 1) if self.off is None else self.off[s:s + 2]
+            if a >= 0:
+                idle[lo:hi] = False
+        bits = lambda t: t.view(torch.int16)        # noqa: E731
+        assert torch.equal(bits(self.Ys)[idle.cuda()], bits(self.before)[idle.cuda()])
+        assert torch.equal(bits(self.Ys[:, :self.ldy]), bits(self.before[:, :self.ldy]))
+
+
+@pytest.mark.parametrize("K,N,r", [(16, 16, 8), (64, 32, 8), (128, 96, 16), (2048, 2048, 16), (144, 80, 24), (48, 272, 40),
+                                   (2880, 2880, 16), (1040, 528, 64), (512, 1536, 128), (4112, 64, 120), (80, 4112, 32)])
+@pytest.mark.parametrize("T", [1, 5])
+def test_single_tokens(T, K, N, r):
+    Case(T, K, N, r, 3, [(2 - i) % 3 for i in range(T)]).run().check()
+
+
+@pytest.mark.parametrize("T", [2, 64, 200, 300])
+def test_many_single_tokens(T):
+    Case(T, 256, 320, 16, 11, [(7 * i) % 12 - 1 for i in range(T)]).run().check()
+
+
+@pytest.mark.parametrize("lens", [[1], [2], [8], [9], [15, 1], [127], [128], [129], [1, 1, 1], [0, 0, 3], [60, 1, 0, 200, 7],
+                                  [16, 16, 16, 16], [300, 1, 1, 1, 500], [1] * 40 + [100]])
+@pytest.mark.parametrize("K,N,r", [(64, 48, 8), (320, 400, 16), (144, 656, 64)])
+def test_packed_requests(lens, K, N, r):
+    off = np.cumsum([0] + lens).tolist()
+    ad = [(5 * i) % 4 - (i % 3 == 2) for i in range(len(lens))]
+    Case(off[-1], K, N, r, 4, ad, off, seed=len(lens)).run().check()
+
+
+@pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 48, 64, 72, 96, 120, 128])
+def test_ranks(r):
+    off = [0, 150, 151, 290]
+    Case(300, 272, 336, r, 2, [1, 0, 1], off).run().check()
+
+
+@pytest.mark.parametrize("lead", [0, 3])
+def test_rows_of_no_request_stay(lead):
+    off = [lead, 40, 40, 170, 200]
+    Case(260, 96, 112, 16, 3, [2, 0, -1, 1], off).run().check()
+
+
+@pytest.mark.parametrize("single", [True, False])
+@pytest.mark.parametrize("ldx,ldy", [(8, 0), (0, 24), (16, 40)])
+def test_strided_rows(single, ldx, ldy):
+    T = 30 if single else 210
+    off = None if single else [0, 5, 200]
+    ad = [i % 3 - 1 for i in range(T)] if single else [1, 0]
+    Case(T, 160, 144, 16, 2, ad, off, ldx=ldx, ldy=ldy).run().check()
+
+
+def test_long_and_wide():
+    Case(3000, 2048, 1536, 16, 4, [0, 3, 1], [0, 1100, 1101, 2990]).run().check()
+    Case(700, 7168, 2048, 32, 2, [1, 0], [0, 350, 700]).run().check()
+
+
+def test_not_finite_rows_keep_to_themselves():
+    for off, ad in (([0, 200], [0]), (None, [0] * 200)):
+        c = Case(200, 128, 96, 16, 1, ad, off)
+        want = Case(200, 128, 96, 16, 1, ad, off).run()
+        c.Xs[17, 3], c.Xs[90, 5], c.Ys[40, 7] = float("nan"), float("inf"), float("inf")
+        c.run()
+        rest = [i for i in range(200) if i not in (17, 90, 40)]
+        assert torch.equal(c.Y[rest], want.Y[rest])
+        assert torch.isnan(c.Y[17]).all() and not torch.isfinite(c.Y[90]).any() and torch.isinf(c.Y[40, 7])
+        assert torch.isfinite(c.Y[40]).sum() == 95
+    # rows without an adapter may hold anything
+    c = Case(20, 64, 64, 8, 1, [0, -1], [0, 10, 20])
+    c.Xs[10:] = float("nan")
+    c.run()
+    assert torch.isfinite(c.Y).all()
+
+
+def test_bad_adapters_and_offsets_are_reported():
+    for off, ad in (([0, 10, 40], [0, 3]), (None, [0] * 39 + [3]), ([0, 30, 20, 40], [0, 1, 2]), ([0, 20, 41], [0, 1]),
+                    ([-5, 20, 40], [0, 1])):
+        c = Case(40, 64, 64, 8, 3, ad, off)
+        with pytest.raises(AssertionError):
+            c.run()
+        assert ml.moe_get_device_error() == ml.MOE_OK
+    c = Case(40, 64, 64, 8, 3, [0, 3], [0, 10, 40])
+    before = c.Y.clone()
+    c.call()
+    torch.cuda.synchronize()
+    assert ml.moe_get_device_error() == ml.MOE_ERR_DEVICE_INDEX
+    assert torch.equal(c.Y[10:], before[10:])
+
+
+def test_no_rows_and_no_adapters():
+    Case(0, 64, 64, 8, 2, []).run()
+    Case(0, 64, 64, 8, 2, [1, 0], [0, 0, 0]).run()
+    Case(9, 64, 64, 8, 0, [-1] * 9).run().check()
+
+
+@pytest.mark.parametrize("off", [None, [0, 1, 150, 151, 280, 300]])
+def test_repeatable_on_streams_and_in_a_graph(off):
+    ad = [i % 4 - 1 for i in range(300)] if off is None else [0, 1, 2, -1, 0]
+    make = lambda: Case(300, 512, 640, 16, 3, ad, off, seed=2)      # noqa: E731
+    want = make().run().Y
+    assert torch.equal(make().run().Y, want)
+    c = make()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    c.call(st)
+    st.synchronize()
+    assert torch.equal(c.Y, want)
+    c = make()
+    start = c.Ys.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.call()
+    for _ in range(2):
+        c.Ys.copy_(start)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c.Y, want)
+
+
+def test_two_calls_on_two_streams():
+    a = Case(500, 256, 512, 16, 3, [0, 1, 2], [0, 100, 300, 500], seed=1)
+    b = Case(64, 256, 512, 32, 5, [i % 5 for i in range(64)], seed=2)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for c in (a, b):
+        c.before = c.Ys.clone()
+    torch.cuda.synchronize()
+    a.call(s1)
+    b.call(s2)
+    torch.cuda.synchronize()
+    assert ml.moe_get_device_error() == ml.MOE_OK
+    a.check()
+    b.check()
+
+
+def test_refusals():
+    z = lambda *s, t=BF: torch.zeros(*s, dtype=t, device="cuda")      # noqa: E731
+    ad, c = z(4, t=torch.int32), z(2, t=torch.float32)
+    ok = dict(X=z(4, 64), adapters=ad, A=z(2, 64, 8), B=z(2, 8, 32), scale=c, Y=z(4, 32))
+    ml.moe_lora_requests(**ok)
+    for kw in (dict(X=z(4, 64, t=torch.float16)), dict(A=z(2, 48, 8)), dict(B=z(2, 16, 32)), dict(B=z(3, 8, 32)),
+               dict(scale=z(2)), dict(Y=z(5, 32)), dict(adapters=z(3, t=torch.int32)), dict(adapters=z(4, t=torch.int64)),
+               dict(X=z(64, 4).t()), dict(A=z(2, 8, 64).transpose(1, 2)), dict(seq_offsets=ad)):
+        with pytest.raises(ValueError):
+            ml.moe_lora_requests(**{**ok, **kw})
+    for kw in (dict(X=z(4, 66)[:, 2:]), dict(Y=z(4, 36)[:, :32]), dict(A=z(2, 64, 12), B=z(2, 12, 32))):
+        with pytest.raises(ml.MoEError):
+            ml.moe_lora_requests(**{**ok, **kw})

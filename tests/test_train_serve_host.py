@@ -1,0 +1,112 @@
+"""Refusals of the balance loss, the AdamW step and the adapters of many requests, on the host
+before any launch (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+import mixture_experts_lora_b200 as ml
+
+P = ctypes.c_void_p
+FAKE, ODD = P(4096), P(4100)       # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    from mixture_experts_lora_b200 import build
+    build.build(quiet=True)
+    return ml.lib()
+
+
+def test_balance_workspace(L):
+    assert ml.moe_balance_workspace_bytes(4096, 128) > 0
+    assert ml.moe_balance_workspace_bytes(0, 8) > 0
+    assert ml.moe_balance_workspace_bytes(4096, 128, 64) > ml.moe_balance_workspace_bytes(4096, 128)
+    for bad in ((-1, 8, 1), (4, 0, 1), (4, 1025, 1), (4, 8, 0), (4, 8, 1 << 24), (1 << 31, 8, 1)):
+        assert ml.moe_balance_workspace_bytes(*bad) == 0
+
+
+def test_balance_loss_refusals(L):
+    def call(T=4, E=8, k=2, off=None, S=1, logits=FAKE, ids=FAKE, loss=FAKE, ws=FAKE, wsb=1 << 30):
+        return L.moe_balance_loss(logits, ids, T, E, k, off, S, None, loss, FAKE, FAKE, ws, wsb, None)
+    assert call(k=0) == call(E=1) == call(k=33, E=64) == call(E=1025) == ml.MOE_ERR_UNSUPPORTED
+    assert call(T=1 << 30, k=2) == call(S=1 << 24, off=FAKE) == ml.MOE_ERR_UNSUPPORTED
+    assert call(T=-1) == call(S=0) == call(S=2) == ml.MOE_ERR_INVALID_ARG      # S = 2 needs offsets
+    assert call(logits=None) == call(ids=None) == call(loss=None) == call(ws=None) == ml.MOE_ERR_INVALID_ARG
+    assert call(ws=ODD) == ml.MOE_ERR_INVALID_ARG
+    assert call(wsb=ml.moe_balance_workspace_bytes(4, 8) - 1) == ml.MOE_ERR_WORKSPACE
+
+
+def test_balance_backward_refusals(L):
+    def call(T=4, E=8, k=2, off=None, S=1, logits=FAKE, counts=FAKE, dloss=FAKE, out=FAKE):
+        return L.moe_balance_loss_backward(logits, counts, FAKE, dloss, T, E, k, off, S, None, out, 0, None)
+    assert call(k=0) == call(E=1) == call(E=1025) == ml.MOE_ERR_UNSUPPORTED
+    assert call(T=-1) == call(S=2) == call(logits=None) == call(counts=None) == ml.MOE_ERR_INVALID_ARG
+    assert call(dloss=None) == call(out=None) == ml.MOE_ERR_INVALID_ARG
+    assert call(T=0, out=None) == ml.MOE_OK
+
+
+def _adamw(L, step=FAKE, n=1, table=True, **kw):
+    cfg = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, param_bf16=1, grad_bf16=1, has_master=0,
+               state_bits=32)
+    row = dict(param=4096, grad=4096, exp_avg=4096, exp_avg_sq=4096, exp_avg_scale=None, exp_avg_sq_scale=None,
+               master=None, size=(1, 1, 64), param_stride=(0, 0, 1), grad_stride=(0, 0, 1))
+    for k, v in kw.items():
+        (cfg if k in cfg else row)[k] = v
+    c = ml.moe_adamw_config_t(**cfg)
+    t = (ml.moe_adamw_tensor_t * 1)()
+    for k, v in row.items():
+        if isinstance(v, tuple):
+            getattr(t[0], k)[:] = v
+        else:
+            setattr(t[0], k, v)
+    return L.moe_adamw_step(t if table else None, n, ctypes.byref(c), None, None, step, 1, None)
+
+
+def test_adamw_refusals(L):
+    bad = ml.MOE_ERR_INVALID_ARG
+    assert _adamw(L, n=-1) == _adamw(L, table=False) == _adamw(L, step=None) == _adamw(L, step=ODD) == bad
+    assert L.moe_adamw_step(None, 0, None, None, None, FAKE, 1, None) == bad
+    for kw in (dict(lr=float("nan")), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.5), dict(eps=-1.0),
+               dict(eps=float("inf")), dict(weight_decay=float("inf")), dict(param=None), dict(grad=None),
+               dict(param=4097), dict(exp_avg=None), dict(exp_avg_sq=4100), dict(size=(1, 1, -1)),
+               dict(param_stride=(0, 0, -1)), dict(param_stride=(0, 0, 0)), dict(state_bits=8),
+               dict(has_master=1), dict(has_master=1, master=4100),
+               dict(param_bf16=0, param=4098), dict(grad_bf16=0, grad=4098)):
+        assert _adamw(L, **kw) == bad, kw
+    for kw in (dict(state_bits=16), dict(param_bf16=0, has_master=1, master=4096), dict(size=(1, 1, 1 << 41)),
+               dict(size=(1 << 16, 1, 1 << 16), param_stride=(1 << 17, 0, 1))):
+        assert _adamw(L, **kw) == ml.MOE_ERR_UNSUPPORTED, kw
+
+
+def test_lora_requests_refusals(L):
+    def call(X=FAKE, ldx=64, off=None, ad=FAKE, T=4, S=4, A=FAKE, B=FAKE, c=FAKE, n=2, K=64, N=32, r=8, Y=FAKE, ldy=32):
+        return L.moe_lora_requests(X, ldx, off, ad, T, S, A, B, c, n, K, N, r, Y, ldy, None)
+    assert call(K=40) == call(K=0) == call(N=24) == call(r=12) == call(r=136) == call(r=0) == ml.MOE_ERR_UNSUPPORTED
+    assert call(T=1 << 24, S=1 << 24) == call(K=1 << 20, ldx=1 << 20) == ml.MOE_ERR_UNSUPPORTED
+    for kw in (dict(T=-1), dict(S=-1), dict(n=-1), dict(S=3), dict(ldx=56), dict(ldx=68), dict(ldy=24), dict(X=None),
+               dict(X=ODD), dict(Y=None), dict(Y=ODD), dict(ad=None), dict(A=None), dict(B=ODD), dict(c=None)):
+        assert call(**kw) == ml.MOE_ERR_INVALID_ARG, kw
+    assert call(T=0, S=0, X=None, Y=None) == ml.MOE_OK
+
+
+def test_bindings_refuse_cpu_tensors_and_wrong_types():
+    z, i = torch.zeros, torch.int32
+    with pytest.raises(ValueError):
+        ml.moe_balance_loss(z(4, 8), z(4, 2, dtype=i), z(1), z(1, 8, dtype=i), z(1, dtype=i), z(1024))
+    with pytest.raises(ValueError):
+        ml.moe_balance_loss(z(4, 8).half(), z(4, 2, dtype=i), z(1), z(1, 8, dtype=i), z(1, dtype=i), z(1024))
+    with pytest.raises(ValueError):
+        ml.moe_balance_loss_backward(z(4, 8), z(1, 8, dtype=i), z(1, dtype=i), z(2), 2, z(4, 8))
+    b = torch.bfloat16
+    with pytest.raises(ValueError):
+        ml.moe_lora_requests(z(4, 64, dtype=b), z(4, dtype=i), z(2, 64, 8, dtype=b), z(2, 8, 32, dtype=b), z(2),
+                             z(4, 32, dtype=b))
+    with pytest.raises(ValueError):
+        ml.moe_lora_requests(z(4, 64), z(4, dtype=i), z(2, 64, 8, dtype=b), z(2, 8, 32, dtype=b), z(2), z(4, 32))
+    with pytest.raises(ValueError):
+        ml.AdamW([z(4)], [z(4)])
+    with pytest.raises(ValueError):
+        ml.AdamW([], [])
+    with pytest.raises(ValueError):
+        ml.AdamW([z(4)], [z(4)], state_bits=4)
