@@ -2,19 +2,33 @@
 //   Y[t] += c_a (X[t] A_a) B_a,   a the adapter of t's request.
 //
 // Reads X once, the adapters in use once, reads and writes Y once: bound by HBM for long
-// prompts, by latency for a few tokens.  A block owns the rows of one request within one
-// window of kRows rows: it sums X A over K in fp32 (each thread eight rank columns of every
-// blockDim-th row of A, joined through shared memory in a fixed order), then adds the
-// product with B to its rows of Y.
+// prompts, by latency for a few tokens.  Two forms:
+//
+// lora_tiles_kernel, for requests of any length.  Rows are cut into windows of 128; a
+// cluster of 1 to 8 CTAs owns the rows of one request within one window and runs both
+// products in one launch, so that X A never leaves the chip:
+//   1. X A: each CTA sums its share of K, 64 columns a stage: TMA brings the rows of X and
+//      64 rows of A, tcgen05.mma adds S[128 x RP] in TMEM;
+//   2. the CTAs' partial S are exchanged through distributed shared memory and summed in
+//      rank order; c S is split into two bf16 (its rounding and what the rounding left) and
+//      written as the K-major operand of the second product, K = 2 RP;
+//   3. each CTA takes its share of the columns, 64 a stage: TMA brings the rows of Y and 64
+//      columns of B, tcgen05.mma forms S B in TMEM, the epilogue warps add it to Y in
+//      shared memory, and TMA stores the rows back.
+// A stage of either product is 16 KB of rows and RP x 64 of the adapter, so both run through
+// one ring of slots, and the first stages of Y and B arrive while X A is still being
+// summed.  The split over a cluster is for batches of few windows: it spreads one window's
+// bytes over as many SMs.  Only 32-row boxes that hold rows of the request are copied; a box
+// that it shares with another request is stored row by row.
+//
+// lora_single_kernel, for one row per request: a cluster of 8 CTAs per row; see there.
 #include "common.cuh"
 #include "internal.h"
 #include "sequences.cuh"
+#include "tmap.cuh"
 
 namespace moe {
 namespace {
-
-constexpr int kThreads = 256;
-constexpr int kRows = 8;
 
 struct LoraArgs {
   const __nv_bfloat16* X;
@@ -32,94 +46,435 @@ struct LoraArgs {
   int* err;
 };
 
-__global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraArgs a) {
+// ---------------------------------------------------------------- rows of one adapter
+template <int RP_>
+struct TilesCfg {
+  static constexpr int RP = RP_;
+  static constexpr int BM = 128, BK = 64, BN = 64;
+  static constexpr int ROWS_BYTES = BM * 64 * 2;          // X or Y rows of a stage
+  static constexpr int AD_BYTES = RP * 64 * 2;            // A or B of a stage
+  static constexpr int STAGE_BYTES = ROWS_BYTES + AD_BYTES;
+  static constexpr int STAGES = RP == 128 ? 3 : 4;
+  static constexpr int OP_ATOMS = RP <= 32 ? 1 : 2 * RP / 64;   // 64-column atoms of [hi | lo]
+  static constexpr int OP_BYTES = OP_ATOMS * BM * 128;
+  static constexpr int PART_BYTES = BM * RP * 4;          // exchanged partial (clusters only)
+  static constexpr int BAR_BYTES = 256;
+  static constexpr int TMEM_COLS = 128;                   // two 64-column accumulators; S before them
+  static constexpr int THREADS = 192;                     // epilogue warps 0-3, loader, MMA issuer
+  static int smem_bytes(bool cluster) {
+    return STAGES * STAGE_BYTES + OP_BYTES + (cluster ? PART_BYTES : 0) + BAR_BYTES + 1024;
+  }
+  // A chunk [64 K rows][RP], rank innermost: rows of up to 128 bytes, two atoms at rank 128
+  static constexpr uint32_t A_SW = RP == 16 ? kSw32 : RP == 32 ? kSw64 : kSw128;
+  static constexpr int A_ROWB = (RP < 64 ? RP : 64) * 2;
+  static constexpr int A_ATOMS = RP > 64 ? 2 : 1;
+  static constexpr int A_ATOM_BYTES = BK * A_ROWB;
+};
+
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS)
+    lora_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
+                      const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmY,
+                      const LoraArgs a) {
+  constexpr int RP = C::RP, S = C::STAGES;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* op = smem + S * C::STAGE_BYTES;                 // [hi | lo] operand of the second product
+  uint64_t* bars = reinterpret_cast<uint64_t*>(op + C::OP_BYTES);
+  float* part = reinterpret_cast<float*>(op + C::OP_BYTES + C::BAR_BYTES);   // clusters only
+  uint64_t* full = bars;                 // [S] TMA bytes of the stage landed
+  uint64_t* xfree = bars + S;            // [S] the MMAs of an X stage completed
+  uint64_t* yfree = bars + 2 * S;        // [S] a Y stage's rows are stored (4 warps)
+  uint64_t* dfull = bars + 3 * S;        // [2] product ready in TMEM
+  uint64_t* dfree = bars + 3 * S + 2;    // [2] product read (4 warps)
+  uint64_t* acc_done = bars + 3 * S + 4;
+  uint64_t* op_ready = bars + 3 * S + 5;
+  uint64_t* drain = bars + 3 * S + 6;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 7);
+
+  const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
+  const int rank = (int)cluster_ctarank(), CL = (int)cluster_nctarank();
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&xfree[i]), 1);
+      mbar_init(smem_u32(&yfree[i]), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&dfull[i]), 1);
+      mbar_init(smem_u32(&dfree[i]), 4);
+    }
+    mbar_init(smem_u32(acc_done), 1);
+    mbar_init(smem_u32(op_ready), C::BM);
+    mbar_init(smem_u32(drain), 1);
+    mbar_fence_init();
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmY);
+  }
+  pdl_begin();
+  // the cluster's tile, the same for all its CTAs: slot -> (window, request) -> rows, adapter
+  const int slot = (int)blockIdx.x / CL;
+  check_offsets(a.off, a.S, a.T, a.err);
+  const int s = block_count_le(a.S, slot, [&](int i) { return (long long)a.off[i] / C::BM + i; }) - 1;
+  if (s < 0) return;
+  const int64_t w = slot - s, lo = a.off[s], hi = a.off[s + 1];
+  const int64_t row0 = w * C::BM;
+  const int64_t r0 = row0 > lo ? row0 : lo, r1 = row0 + C::BM < hi ? row0 + C::BM : hi;
+  if (lo < 0 || r1 > a.T || r0 >= r1) return;
+  const int ad = a.adapters[s];
+  if (ad < 0) return;
+  if (ad >= a.n_adapters) {
+    if (tid == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
+    return;
+  }
+  // 32-row boxes that hold rows of the request
+  const int box0 = (int)(r0 - row0) / 32, box1 = (int)(r1 - 1 - row0) / 32 + 1;
+  const int nk = (a.K + C::BK - 1) / C::BK, nn = (a.N + C::BN - 1) / C::BN;
+  const int n_x = (nk - rank + CL - 1) / CL;      // this CTA's stages: rank, rank + CL, ...
+  const int n_y = rank < nn ? (nn - rank + CL - 1) / CL : 0;
+
+  if (warp == 5) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ loader
+    if (CL > 1) cluster_arrive();
+    if (lane == 0) {
+      const uint32_t bytes = (uint32_t)(box1 - box0) * 32 * 128 + C::AD_BYTES;
+      int it = 0;
+      for (; it < n_x + n_y; ++it) {
+        const int st = it % S;
+        if (it >= S) {
+          // the slot's last stage was an X stage (its MMAs read it) or a Y stage (stored)
+          const int prev = it - S;
+          if (prev < n_x) ok = mbar_wait(smem_u32(&xfree[st]), (prev / S) & 1, a.err);
+          else {
+            // uses of this slot by Y stages: the first is the smallest j >= n_x, j % S == st
+            const int first = n_x + ((st - n_x) % S + S) % S;
+            ok = mbar_wait(smem_u32(&yfree[st]), ((prev - first) / S) & 1, a.err);
+          }
+          if (!ok) break;
+        }
+        uint8_t* p = smem + st * C::STAGE_BYTES;
+        const uint32_t fb = smem_u32(&full[st]), rows = smem_u32(p), adp = smem_u32(p + C::ROWS_BYTES);
+        mbar_arrive_expect_tx(fb, bytes);
+        if (it < n_x) {
+          const int k0 = (rank + it * CL) * C::BK;
+#pragma unroll
+          for (int x = 0; x < C::A_ATOMS; ++x) tma_load_3d(&tmA, fb, adp + x * C::A_ATOM_BYTES, x * 64, k0, ad);
+          for (int b = box0; b < box1; ++b) tma_load_2d(&tmX, fb, rows + b * 4096, k0, (int)row0 + b * 32);
+        } else {
+          const int n0 = (rank + (it - n_x) * CL) * C::BN;
+          tma_load_3d(&tmB, fb, adp, n0, 0, ad);
+          for (int b = box0; b < box1; ++b) tma_load_2d(&tmY, fb, rows + b * 4096, n0, (int)row0 + b * 32);
+        }
+      }
+      // after a failed wait, the copies on their way land before the CTA ends
+      for (int j = it < S ? 0 : it - S; !ok && j < it; ++j) mbar_wait(smem_u32(&full[j % S]), (j / S) & 1, a.err);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA issuer
+    if (CL > 1) cluster_arrive();
+    if (lane == 0) {
+      const uint32_t id1 = idesc_bf16(128, RP, 0, 1), id2 = idesc_bf16(128, C::BN, 0, 1);
+      for (int it = 0; it < n_x && ok; ++it) {
+        const int st = it % S;
+        ok = mbar_wait(smem_u32(&full[st]), (it / S) & 1, a.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t rows = smem_u32(smem + st * C::STAGE_BYTES), adp = rows + C::ROWS_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < C::BK / 16; ++kk)
+          umma_bf16(tmem, smem_desc(rows + kk * 32, 16, 1024, kSw128),
+                    smem_desc(adp + kk * 16 * C::A_ROWB, C::A_ATOM_BYTES, 8 * C::A_ROWB, C::A_SW), id1,
+                    (it | kk) ? 1u : 0u);
+        umma_commit(smem_u32(&xfree[st]));
+      }
+      umma_commit(smem_u32(acc_done));
+      if (ok && n_y > 0) ok = mbar_wait(smem_u32(op_ready), 0, a.err);
+      tc_fence_after();
+      for (int j = 0; j < n_y && ok; ++j) {
+        const int it = n_x + j, st = it % S, d = j & 1;
+        ok = mbar_wait(smem_u32(&full[st]), (it / S) & 1, a.err);
+        if (ok && j >= 2) ok = mbar_wait(smem_u32(&dfree[d]), ((j - 2) / 2) & 1, a.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t adp = smem_u32(smem + st * C::STAGE_BYTES + C::ROWS_BYTES), opb = smem_u32(op);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int kk = 0; kk < RP / 16; ++kk) {
+            const int col = h * RP + kk * 16;
+            umma_bf16(tmem + d * C::BN, smem_desc(opb + (col / 64) * (C::BM * 128) + (col % 64) * 2, 16, 1024, kSw128),
+                      smem_desc(adp + kk * 16 * 128, RP * 128, 1024, kSw128), id2, (h | kk) ? 1u : 0u);
+          }
+        umma_commit(smem_u32(&dfull[d]));
+      }
+      if (!ok) {       // the MMAs on their way are done before TMEM is freed
+        umma_commit(smem_u32(drain));
+        mbar_wait(smem_u32(drain), 0, a.err);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue warps: tile row = tid
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const bool mine = warp >= box0 && warp < box1;         // this warp's box holds rows
+    ok = mbar_wait(smem_u32(acc_done), 0, a.err);
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after();
+    const float c = a.scale[ad];
+    // partial S in 16-byte pieces, piece g of row t at g ^ (t mod pieces): the rows' banks differ
+    constexpr int PIECES = RP / 4;
+    if (CL > 1) {
+#pragma unroll
+      for (int c0 = 0; c0 < RP; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld16(lanes + c0, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<uint4*>(part + tid * RP + (((c0 / 4 + g) ^ (tid & (PIECES - 1))) * 4)) =
+              make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+      }
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+    }
+#pragma unroll 1
+    for (int c0 = 0; c0 < RP; c0 += 16) {
+      float x[16];
+      if (CL > 1) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = 0.f;
+        for (int q = 0; q < CL; ++q) {
+          const uint32_t base = mapa_smem(smem_u32(part + tid * RP), (uint32_t)q);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float4 v = ld_cluster_f4(base + (((c0 / 4 + g) ^ (tid & (PIECES - 1))) * 16));
+            x[4 * g] += v.x; x[4 * g + 1] += v.y; x[4 * g + 2] += v.z; x[4 * g + 3] += v.w;
+          }
+        }
+      } else {
+        uint32_t v[16];
+        tmem_ld16(lanes + c0, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float h[8], l[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float v = x[8 * g + i] * c;
+          h[i] = __bfloat162float(__float2bfloat16_rn(v));
+          l[i] = isinf(h[i]) ? 0.f : v - h[i];
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int col = p * RP + c0 + 8 * g, chunk = (col % 64) / 8;
+          *reinterpret_cast<uint4*>(op + (col / 64) * (C::BM * 128) + tid * 128 + ((chunk ^ (tid & 7)) << 4)) =
+              pack8(p == 0 ? h : l);
+        }
+      }
+    }
+    tc_fence_before();
+    fence_proxy_async_smem();
+    mbar_arrive(smem_u32(op_ready));
+    const int64_t brow = row0 + warp * 32;                 // first row of this warp's box
+    const bool whole = mine && brow >= r0 && brow + 32 <= r1;
+    for (int j = 0; j < n_y; ++j) {
+      const int it = n_x + j, st = it % S, d = j & 1;
+      if (ok) ok = mbar_wait(smem_u32(&dfull[d]), (j / 2) & 1, a.err);
+      if (ok) ok = mbar_wait(smem_u32(&full[st]), (it / S) & 1, a.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint8_t* rows = smem + st * C::STAGE_BYTES;
+      const int n0 = (rank + j * CL) * C::BN;
+      if (mine) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[32];
+          tmem_ld32(lanes + d * C::BN + half * 32, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint4* p = reinterpret_cast<uint4*>(rows + tid * 128 + (((half * 4 + g) ^ (tid & 7)) << 4));
+            float y[8];
+            unpack8(*p, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] += __uint_as_float(v[8 * g + i]);
+            *p = pack8(y);
+          }
+        }
+      }
+      tc_fence_before();
+      if (whole) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&dfree[d]));
+          tma_store_2d(&tmY, smem_u32(rows + warp * 4096), n0, (int)brow);
+          bulk_commit_group();
+          bulk_wait_read<0>();
+          mbar_arrive(smem_u32(&yfree[st]));
+        }
+      } else {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&dfree[d]));
+        if (mine) {
+          // four rows at a time, eight lanes a row
+          for (int i = 0; i < 32; i += 4) {
+            const int t = warp * 32 + i + lane / 8, g = lane & 7, n = n0 + g * 8;
+            const int64_t row = row0 + t;
+            if (row >= r0 && row < r1 && n < a.N)
+              *reinterpret_cast<uint4*>(a.Y + row * a.ldy + n) =
+                  *reinterpret_cast<const uint4*>(rows + t * 128 + ((g ^ (t & 7)) << 4));
+          }
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(smem_u32(&yfree[st]));
+      }
+    }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
+  }
+  // everybody is done with its own pipes, and with the others' partials
+  if (CL > 1) {
+    if (warp >= 4) cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int RP>
+cudaError_t launch_tiles(const LoraArgs& a, int CL, cudaStream_t s) {
+  using C = TilesCfg<RP>;
+  CUtensorMap tx, ta, tb, ty;
+  // (without adapters nothing reads the maps of A and B: any valid tensor does)
+  const bool none = a.n_adapters == 0;
+  const uint64_t n = none ? 1 : (uint64_t)a.n_adapters;
+  const void* A = none ? a.X : a.A;
+  const void* B = none ? a.X : a.B;
+  if (!encode2d(&tx, a.X, (uint64_t)a.T, (uint64_t)a.K, (uint64_t)a.ldx, 32, 64) ||
+      !encode2d(&ty, a.Y, (uint64_t)a.T, (uint64_t)a.N, (uint64_t)a.ldy, 32, 64) ||
+      !encode3d(&ta, A, n, (uint64_t)a.K, (uint64_t)a.r, 64, RP < 64 ? RP : 64) ||
+      !encode3d(&tb, B, n, (uint64_t)a.r, (uint64_t)a.N, RP, 64))
+    return cudaErrorInvalidValue;
+  const int smem = C::smem_bytes(CL > 1);
+  auto kern = lora_tiles_kernel<C>;
+  cudaError_t st = ensure_smem(kern, C::smem_bytes(true));
+  if (st != cudaSuccess) return st;
+  const int64_t slots = (a.T + C::BM - 1) / C::BM + a.S - 1;
+  ProfScope ps(K_LORA_REQUESTS, s);
+  return launch_pdl(kern, dim3((unsigned)(slots * CL)), dim3(C::THREADS), smem, s, CL, tx, ta, tb, ty, a);
+}
+
+// CTAs per cluster: as many as keep the windows' clusters within two CTAs per SM (the
+// occupancy at rank 16), and no more than there are 64-column stages of K to share.
+int cluster_size(int64_t T, int K) {
+  const int64_t tiles = (T + 127) / 128;
+  int cl = 1;
+  while (cl < 8 && tiles * cl * 2 <= 2 * (int64_t)device_sms() && cl * 2 <= (K + 63) / 64) cl *= 2;
+  return cl;
+}
+
+// ---------------------------------------------------------------- one row per request
+constexpr int kThreads = 256;
+
+__global__ void __launch_bounds__(kThreads) lora_single_kernel(const LoraArgs a) {
   pdl_begin();
   __shared__ float s_red[kThreads * 8];
-  __shared__ float s_xa[kRows * 128];
-  int s = blockIdx.x;
-  int64_t r0 = s, r1 = s + 1;
-  if (a.off != nullptr) {
-    check_offsets(a.off, a.S, a.T, a.err);
-    // the slot's sequence: the last whose first slot is not past it
-    s = block_count_le(a.S, blockIdx.x, [&](int i) { return (long long)a.off[i] / kRows + i; }) - 1;
-    if (s < 0) return;
-    const int64_t w = (int64_t)blockIdx.x - s, lo = a.off[s], hi = a.off[s + 1];
-    r0 = w * kRows > lo ? w * kRows : lo;
-    r1 = (w + 1) * kRows < hi ? (w + 1) * kRows : hi;
-    if (lo < 0 || r1 > a.T || r0 >= r1) return;
-  }
-  const int ad = a.adapters[s];
+  __shared__ float s_xa[128];
+  const int64_t row = blockIdx.x;
+  const int ad = a.adapters[row];
   if (ad < 0) return;
   if (ad >= a.n_adapters) {
     if (threadIdx.x == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
     return;
   }
-  const int nr = (int)(r1 - r0), tid = threadIdx.x;
+  const int tid = threadIdx.x;
   const int groups = a.r / 8, lanes = kThreads / groups;     // rank groups of 8, rows of A at a time
   const int g = tid % groups, kl = tid / groups;
   const __nv_bfloat16* A = a.A + (int64_t)ad * a.K * a.r;
   const __nv_bfloat16* B = a.B + (int64_t)ad * a.r * a.N;
-  const __nv_bfloat16* X = a.X + r0 * a.ldx;
-  float acc[kRows][8];
+  const __nv_bfloat16* X = a.X + row * a.ldx;
+  float acc[8];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i)
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[i][c] = 0.f;
+  for (int c = 0; c < 8; ++c) acc[c] = 0.f;
   if (kl < lanes) {
     for (int k = kl; k < a.K; k += lanes) {
       float v[8];
       unpack8(*reinterpret_cast<const uint4*>(A + (int64_t)k * a.r + g * 8), v);
+      const float x = __bfloat162float(X[k]);
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        if (i >= nr) break;
-        const float x = __bfloat162float(X[i * a.ldx + k]);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) acc[i][c] += x * v[c];
-      }
+      for (int c = 0; c < 8; ++c) acc[c] += x * v[c];
     }
   }
-  const float scale = a.scale[ad];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    if (i >= nr) break;
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < 8; ++c) s_red[tid * 8 + c] = acc[i][c];
-    __syncthreads();
-    if (tid < a.r) {
-      float sum = 0.f;
-      for (int l = 0; l < lanes; ++l) sum += s_red[(l * groups + tid / 8) * 8 + (tid & 7)];
-      s_xa[i * 128 + tid] = sum * scale;
-    }
+  for (int c = 0; c < 8; ++c) s_red[tid * 8 + c] = acc[c];
+  __syncthreads();
+  if (tid < a.r) {
+    float sum = 0.f;
+    for (int l = 0; l < lanes; ++l) sum += s_red[(l * groups + tid / 8) * 8 + (tid & 7)];
+    s_xa[tid] = sum * a.scale[ad];
   }
   __syncthreads();
   for (int n = tid * 8; n < a.N; n += kThreads * 8) {
-    float y[kRows][8];
+    uint4* p = reinterpret_cast<uint4*>(a.Y + row * a.ldy + n);
+    float y[8], v[8];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
-#pragma unroll
-      for (int c = 0; c < 8; ++c) y[i][c] = 0.f;
+    for (int c = 0; c < 8; ++c) y[c] = 0.f;
     for (int j = 0; j < a.r; ++j) {
-      float v[8];
       unpack8(*reinterpret_cast<const uint4*>(B + (int64_t)j * a.N + n), v);
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        if (i >= nr) break;
-        const float x = s_xa[i * 128 + j];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) y[i][c] += x * v[c];
-      }
+      for (int c = 0; c < 8; ++c) y[c] += s_xa[j] * v[c];
     }
+    unpack8(*p, v);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (i >= nr) break;
-      uint4* p = reinterpret_cast<uint4*>(a.Y + (r0 + i) * a.ldy + n);
-      float v[8];
-      unpack8(*p, v);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] += y[i][c];
-      *p = pack8(v);
-    }
+    for (int c = 0; c < 8; ++c) v[c] += y[c];
+    *p = pack8(v);
   }
 }
 
@@ -161,9 +516,15 @@ extern "C" moe_status_t moe_lora_requests(const moe_bf16_t* X, int64_t ldx, cons
   a.err = moe_status_word();
   if (a.err == nullptr) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int64_t blocks = seq_offsets == nullptr ? S : (T + kRows - 1) / kRows + S;
-  ProfScope ps(K_LORA_REQUESTS, s);
-  if (launch_pdl(lora_rows_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, 1, a) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  cudaError_t e;
+  if (seq_offsets == nullptr) {
+    ProfScope ps(K_LORA_REQUESTS, s);
+    e = launch_pdl(lora_single_kernel, dim3((unsigned)S), dim3(kThreads), 0, s, 1, a);
+  } else {
+    const int cl = cluster_size(T, K);
+    e = r <= 16 ? launch_tiles<16>(a, cl, s) : r <= 32 ? launch_tiles<32>(a, cl, s)
+        : r <= 64 ? launch_tiles<64>(a, cl, s) : launch_tiles<128>(a, cl, s);
+  }
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
