@@ -38,6 +38,7 @@ struct Tensor {
   float* vs;
   int64_t n;
   uint32_t d1, d2;         // strided views: sizes of the two inner dimensions; d2 = 0: contiguous
+  bool vec;                // groups of eight elements lie together, 16-byte aligned
   int64_t ps[3], gs[3];
 };
 
@@ -59,36 +60,52 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// Largest |value| of the warp's elements; a NaN among them wins.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// e4m3 code of x (x >= 0), |x| inv <= 448: moving e4m3's exponents to the bottom of fp32's
-// (times 2^-120) makes e4m3's subnormals fp32's own, after which 20 mantissa bits go.
+// e4m3 code of y = x inv (x >= 0, y <= 448): moving e4m3's exponents to the bottom of fp32's
+// (times 2^-120) makes e4m3's subnormals fp32's own, after which 20 mantissa bits go.  A y
+// past 448 by a rounding stays the largest code.
 __device__ __forceinline__ uint32_t encode_abs(float x, float inv, uint32_t rnd16) {
   const uint32_t bits = __float_as_uint(__fmul_rn(__fmul_rn(x, inv), 0x1p-120f));
   const uint32_t c = (bits + (rnd16 << 4)) >> 20;
   return c < 0x7Eu ? c : 0x7Eu;
 }
 
-__device__ __forceinline__ float decode(uint8_t c) {
-  __nv_fp8_e4m3 q;
-  q.__x = c;
-  return static_cast<float>(q);
+// Two codes (the low bytes) as floats; e4m3 to fp16 and fp32 is exact.
+__device__ __forceinline__ float2 decode2(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 template <bool BF16>
-__device__ __forceinline__ float load_as_float(const void* p, int64_t i) {
+__device__ __forceinline__ float load_one(const void* p, int64_t i) {
   if constexpr (BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
   else return static_cast<const float*>(p)[i];
 }
 template <bool BF16>
-__device__ __forceinline__ void store_float(void* p, int64_t i, float v) {
+__device__ __forceinline__ void store_one(void* p, int64_t i, float v) {
   if constexpr (BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
   else static_cast<float*>(p)[i] = v;
+}
+// Eight consecutive elements from a 16-byte aligned place.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
+  if constexpr (BF16) {
+    unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i), x);
+  } else {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 u = q[0], v = q[1];
+    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&x)[8]) {
+  if constexpr (BF16) {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = pack8(x);
+  } else {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    q[0] = make_float4(x[0], x[1], x[2], x[3]);
+    q[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
 }
 
 // Offset of element i (row-major index of the view) under strides st.
@@ -98,18 +115,31 @@ __device__ __forceinline__ int64_t view_offset(const Tensor& t, int64_t i, const
   return a * st[0] + b * st[1] + c * st[2];
 }
 
+// The scalars of a step.
+struct Step {
+  float b1, b2, one_b1, one_b2, eps, gscale, c1, rbc2, keep;
+};
+
+// One element.  The moments are rounded operation by operation (no fused multiply-adds), as
+// separate fp32 operations elsewhere round them: 8-bit codes then agree bit for bit.
+__device__ __forceinline__ void update(const Step& q, float g, float& m, float& v, float& root, float& w) {
+  g = __fmul_rn(g, q.gscale);
+  m = __fadd_rn(__fmul_rn(q.b1, m), __fmul_rn(q.one_b1, g));
+  v = __fadd_rn(__fmul_rn(q.b2, v), __fmul_rn(q.one_b2, __fmul_rn(g, g)));
+  root = __fsqrt_rn(v);
+  w = w * q.keep - q.c1 * (m / (root * q.rbc2 + q.eps));
+}
+
 template <int NT, bool PBF16, bool GBF16, bool MASTER, bool BITS8>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwArgs<NT> a) {
   pdl_begin();
   const int lane = lane_id();
   const long long t_step = a.step[0] + 1;
   const float lr = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
-  const float gscale = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
   // 1 - b^t = -expm1(t ln b): relative accuracy even where b^t is near 1
   const float tf = (float)t_step;
-  const float c1 = lr / -expm1f(tf * a.ln_b1);
-  const float rbc2 = 1.0f / sqrtf(-expm1f(tf * a.ln_b2));
-  const float keep = 1.0f - lr * a.wd;
+  const Step q = {a.b1, a.b2, a.one_b1, a.one_b2, a.eps, a.grad_scale != nullptr ? *a.grad_scale : 1.0f,
+                  lr / -expm1f(tf * a.ln_b1), 1.0f / sqrtf(-expm1f(tf * a.ln_b2)), 1.0f - lr * a.wd};
   const uint32_t seed = mix32((uint32_t)t_step);
   const int n_chunks = a.chunk0[a.n];
   for (int c = blockIdx.x; c < n_chunks; c += gridDim.x) {
@@ -124,65 +154,110 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const int64_t blk = base / kBlockElems;
     float msc = 0.f, vsc = 0.f;
     if constexpr (BITS8) { msc = t.ms[blk]; vsc = t.vs[blk]; }
-    float m[8], u[8];
-    float mtop = 0.f, vtop = 0.f;
+    // lane's elements: eight in a row where 16-byte accesses are possible (first = base +
+    // 8 lane, step 1), else every 32nd (first = base + lane, step 32)
+    const int64_t first = t.vec ? base + 8 * lane : base + lane;
+    const int step = t.vec ? 1 : 32;
+    float m[8], v[8], u[8], w[8], g[8];
+    const bool whole = t.vec && first + 8 <= t.n;
+    if (whole) {
+      const int64_t po = view_offset(t, first, t.ps);
+      load8<GBF16>(t.g, view_offset(t, first, t.gs), g);
+      if constexpr (MASTER) load8<false>(t.w, first, w);
+      else load8<PBF16>(t.p, po, w);
+      if constexpr (BITS8) {
+        const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + first);
+        const uint2 cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + first);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t i = base + 32 * j + lane;
-      m[j] = u[j] = 0.f;
-      if (i >= t.n) continue;
-      const int64_t po = view_offset(t, i, t.ps);
-      const float g = load_as_float<GBF16>(t.g, view_offset(t, i, t.gs)) * gscale;
-      float mi, vi;
-      if constexpr (BITS8) {
-        mi = decode(static_cast<const uint8_t*>(t.m)[i]) * msc;
-        vi = decode(static_cast<const uint8_t*>(t.v)[i]) * vsc;
-        vi *= vi;
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = decode2((j < 2 ? cm.x : cm.y) >> (16 * (j & 1)) & 0xffffu);
+          const float2 y = decode2((j < 2 ? cv.x : cv.y) >> (16 * (j & 1)) & 0xffffu);
+          m[2 * j] = __fmul_rn(x.x, msc);
+          m[2 * j + 1] = __fmul_rn(x.y, msc);
+          const float y0 = __fmul_rn(y.x, vsc), y1 = __fmul_rn(y.y, vsc);
+          v[2 * j] = __fmul_rn(y0, y0);
+          v[2 * j + 1] = __fmul_rn(y1, y1);
+        }
       } else {
-        mi = static_cast<const float*>(t.m)[i];
-        vi = static_cast<const float*>(t.v)[i];
+        load8<false>(t.m, first, m);
+        load8<false>(t.v, first, v);
       }
-      mi = a.b1 * mi + a.one_b1 * g;
-      vi = a.b2 * vi + a.one_b2 * (g * g);
-      const float root = sqrtf(vi);
-      float w = MASTER ? t.w[i] : load_as_float<PBF16>(t.p, po);
-      w = w * keep - c1 * (mi / (root * rbc2 + a.eps));
-      if constexpr (MASTER) t.w[i] = w;
-      store_float<PBF16>(t.p, po, w);
-      if constexpr (BITS8) {
-        m[j] = mi;
-        u[j] = root;
-        mtop = max_nan(mtop, fabsf(mi));
-        vtop = max_nan(vtop, root);
-      } else {
-        static_cast<float*>(t.m)[i] = mi;
-        static_cast<float*>(t.v)[i] = vi;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) update(q, g[j], m[j], v[j], u[j], w[j]);
+      if constexpr (MASTER) store8<false>(t.w, first, w);
+      store8<PBF16>(t.p, po, w);
+      if constexpr (!BITS8) {
+        store8<false>(t.m, first, m);
+        store8<false>(t.v, first, v);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t i = first + j * step;
+        m[j] = u[j] = 0.f;
+        if (i >= t.n) continue;
+        const int64_t po = view_offset(t, i, t.ps);
+        const float gj = load_one<GBF16>(t.g, view_offset(t, i, t.gs));
+        float vj, wj;
+        if constexpr (MASTER) wj = t.w[i];
+        else wj = load_one<PBF16>(t.p, po);
+        if constexpr (BITS8) {
+          m[j] = __fmul_rn(decode2(static_cast<const uint8_t*>(t.m)[i]).x, msc);
+          vj = __fmul_rn(decode2(static_cast<const uint8_t*>(t.v)[i]).x, vsc);
+          vj = __fmul_rn(vj, vj);
+        } else {
+          m[j] = static_cast<const float*>(t.m)[i];
+          vj = static_cast<const float*>(t.v)[i];
+        }
+        update(q, gj, m[j], vj, u[j], wj);
+        if constexpr (MASTER) t.w[i] = wj;
+        store_one<PBF16>(t.p, po, wj);
+        if constexpr (!BITS8) {
+          static_cast<float*>(t.m)[i] = m[j];
+          static_cast<float*>(t.v)[i] = vj;
+        }
       }
     }
     if constexpr (BITS8) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        mtop = max_nan(mtop, __shfl_xor_sync(0xffffffffu, mtop, o));
-        vtop = max_nan(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
-      }
-      if (mtop < 0x1p-100f) mtop = 0.f;
-      if (vtop < 0x1p-100f) vtop = 0.f;
-      const float minv = mtop == 0.f ? 0.f : 448.0f / mtop, vinv = vtop == 0.f ? 0.f : 448.0f / vtop;
+      // non-negative floats order as their bits, a NaN above all
+      uint32_t mb = 0, vb = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int64_t i = base + 32 * j + lane;
-        const uint32_t h = mix32((uint32_t)i ^ seed);
-        uint32_t cm = encode_abs(fabsf(m[j]), minv, h & 0xffffu);
-        if (m[j] < 0.f && cm != 0) cm |= 0x80u;
-        uint32_t cv = encode_abs(u[j], vinv, h >> 16);
-        if (u[j] > 0.f && vinv != 0.f && cv == 0) cv = 1u;
-        // (the codes' memory is whole blocks)
-        static_cast<uint8_t*>(t.m)[i] = (uint8_t)cm;
-        static_cast<uint8_t*>(t.v)[i] = (uint8_t)cv;
+        mb = max(mb, __float_as_uint(m[j]) & 0x7fffffffu);
+        vb = max(vb, __float_as_uint(u[j]) & 0x7fffffffu);
+      }
+      float mtop = __uint_as_float(__reduce_max_sync(0xffffffffu, mb));
+      float vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, vb));
+      if (mtop < 0x1p-100f) mtop = 0.f;
+      if (vtop < 0x1p-100f) vtop = 0.f;
+      const float minv = mtop == 0.f ? 0.f : __fmul_rn(__frcp_rn(mtop), 448.0f);
+      const float vinv = vtop == 0.f ? 0.f : __fmul_rn(__frcp_rn(vtop), 448.0f);
+      uint32_t cm[8], cv[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t h = mix32((uint32_t)(first + j * step) ^ seed);
+        cm[j] = encode_abs(fabsf(m[j]), minv, h & 0xffffu);
+        if (cm[j] != 0) cm[j] |= (__float_as_uint(m[j]) >> 24) & 0x80u;
+        cv[j] = encode_abs(u[j], vinv, h >> 16);
+        if (u[j] > 0.f && vinv != 0.f && cv[j] == 0) cv[j] = 1u;
+      }
+      // (the codes' memory is whole blocks: no end to look at)
+      uint8_t* dm = static_cast<uint8_t*>(t.m) + first;
+      uint8_t* dv = static_cast<uint8_t*>(t.v) + first;
+      if (t.vec) {
+        const auto pack = [](const uint32_t* c) { return c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24; };
+        *reinterpret_cast<uint2*>(dm) = make_uint2(pack(cm), pack(cm + 4));
+        *reinterpret_cast<uint2*>(dv) = make_uint2(pack(cv), pack(cv + 4));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          dm[32 * j] = (uint8_t)cm[j];
+          dv[32 * j] = (uint8_t)cv[j];
+        }
       }
       if (lane == 0) {
-        t.ms[blk] = mtop / 448.0f;
-        t.vs[blk] = vtop / 448.0f;
+        t.ms[blk] = __fmul_rn(mtop, 1.0f / 448.0f);
+        t.vs[blk] = __fmul_rn(vtop, 1.0f / 448.0f);
       }
     }
   }
@@ -214,6 +289,13 @@ cudaError_t launch(const moe_adamw_tensor_t* src, int n, const moe_adamw_config_
     d.d1 = (uint32_t)t.size[1];
     d.d2 = flat ? 0u : (uint32_t)t.size[2];
     for (int k = 0; k < 3; ++k) { d.ps[k] = t.param_stride[k]; d.gs[k] = t.grad_stride[k]; }
+    // 16-byte accesses to groups of eight: aligned bases, and in a strided view rows of whole
+    // groups that begin aligned
+    const int pe = P ? 8 : 4, ge = G ? 8 : 4;             // elements in 16 bytes
+    d.vec = aligned16(t.param) && aligned16(t.grad) &&
+            (flat || (t.size[2] % 8 == 0 && t.param_stride[2] == 1 && t.grad_stride[2] == 1 &&
+                      t.param_stride[0] % pe == 0 && t.param_stride[1] % pe == 0 &&
+                      t.grad_stride[0] % ge == 0 && t.grad_stride[1] % ge == 0));
     a.chunk0[i] = (int32_t)chunks;
     chunks += (d.n + kChunk - 1) / kChunk;
   }
@@ -235,7 +317,7 @@ cudaError_t launch(const moe_adamw_tensor_t* src, int n, const moe_adamw_config_
 
 // Tensors per launch: a short table for few (kernel parameters are copied at every launch),
 // a long one that fills the 32764 bytes that a kernel's parameters may take.
-constexpr int kShort = 16, kLong = 256;
+constexpr int kShort = 16, kLong = 240;
 static_assert(sizeof(AdamwArgs<kLong>) <= 32764, "kernel parameters");
 
 template <bool P, bool G, bool M, bool B8>

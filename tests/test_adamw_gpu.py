@@ -2,7 +2,8 @@
 
 Bounds (u = 2^-24): m and v are two products and a sum, 4 u of the summands' absolute values
 (6 u for v, whose gradient is squared); the update is a handful of fp32 operations and two
-expm1 (a few u each), 64 u of its value; w adds 4 u of itself.  A bf16 weight adds half a bf16
+expm1 (a few u each) on m, 64 u of what it would be if m's summands did not cancel; w adds 6 u
+of itself.  A bf16 weight adds half a bf16
 step, 2^-8 of its value.
 
 8 bits: x (m or sqrt(v)) is off by e <= 4 u (|b1 m0| + |(1 - b1) g|) (m's summands may cancel,
@@ -61,7 +62,8 @@ class Mirror:
                 continue
             g = g * scale
             w, m, v = O.adamw(w0, g, m0, v0, self.t, lr, b1, b2, hyper["eps"], hyper["weight_decay"])
-            upd = np.abs(w - w0 * (1 - lr * hyper["weight_decay"]))
+            # m's error is a share of its summands, which may cancel in m itself
+            upd = np.abs(O.adamw(0.0, np.abs(g), np.abs(m0), v0, self.t, lr, b1, b2, hyper["eps"], 0.0)[0])
             tol = 64 * U * upd + 6 * U * np.abs(w0)
             p = o.params[i]
             if o.master is not None and p.dtype == BF:

@@ -59,8 +59,10 @@ def test_training_steps(bits, graph):
         for i, name in enumerate(ADAPTERS):
             w, _, _ = O.adamw(master[i], to_np(opt.grads[i]), mom[i][0], mom[i][1], t, 1e-3, 0.9, 0.999, 1e-8, 0.01)
             got = to_np(opt._part(opt.master, i))
-            # 64 u of an update of about lr, 6 u of the weight
-            assert np.all(np.abs(got - w) <= 2.0 ** -24 * (64 * np.abs(w - master[i]) + 6 * np.abs(w)) + 1e-12)
+            # 64 u of the update if m's summands did not cancel, 6 u of the weight (test_adamw_gpu.py)
+            upd = O.adamw(0.0, np.abs(to_np(opt.grads[i])), np.abs(mom[i][0]), mom[i][1], t, 1e-3, 0.9, 0.999, 1e-8, 0.0)[0]
+            past = np.abs(got - w) - 2.0 ** -24 * (64 * np.abs(upd) + 6 * np.abs(w)) - 1e-12
+            assert past.max() <= 0
             assert torch.equal(inp[name], opt._part(opt.master, i).to(torch.bfloat16))
             assert not np.array_equal(w, master[i])
 
