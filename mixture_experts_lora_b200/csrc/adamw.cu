@@ -60,13 +60,28 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// e4m3 code of y = x inv (x >= 0, y <= 448): moving e4m3's exponents to the bottom of fp32's
-// (times 2^-120) makes e4m3's subnormals fp32's own, after which 20 mantissa bits go.  A y
-// past 448 by a rounding stays the largest code.
-__device__ __forceinline__ uint32_t encode_abs(float x, float inv, uint32_t rnd16) {
-  const uint32_t bits = __float_as_uint(__fmul_rn(__fmul_rn(x, inv), 0x1p-120f));
-  const uint32_t c = (bits + (rnd16 << 4)) >> 20;
-  return c < 0x7Eu ? c : 0x7Eu;
+// e4m3 code of y = |x| inv, 0 <= y <= 448, in the low bits of the top byte: moving e4m3's
+// exponents to the bottom of fp32's (times 2^-120) makes e4m3's subnormals fp32's own, after
+// which the low 20 mantissa bits are what is rounded: up if they and 20 random bits (16 and
+// zeros) carry.
+__device__ __forceinline__ uint32_t encode_top(float x, float inv, uint32_t rnd16) {
+  return (__float_as_uint(__fmul_rn(fabsf(__fmul_rn(x, inv)), 0x1p-120f)) + rnd16 * 16u) << 4;
+}
+// The top bytes of four words.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+// 0x80 in every byte that is not zero (bytes up to 0x80).
+__device__ __forceinline__ uint32_t nonzero_bytes(uint32_t w) { return (w + 0x7f7f7f7fu) & 0x80808080u; }
+
+// The rounded square root of a normal v: one Newton step (v - s^2) / (2 s) from s = v rsqrt(v).
+// Equal to __fsqrt_rn for all 2^24 values of [1, 4) (and so for their scalings by 4^k), in half
+// its instructions: the 8-bit step is bound by instruction issue.
+__device__ __forceinline__ float root_normal(float v) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  const float s = __fmul_rn(v, r);
+  return __fmaf_rn(__fmaf_rn(-s, s, v), 0.5f * r, s);
 }
 
 // Two codes (the low bytes) as floats; e4m3 to fp16 and fp32 is exact.
@@ -122,12 +137,14 @@ struct Step {
 
 // One element.  The moments are rounded operation by operation (no fused multiply-adds), as
 // separate fp32 operations elsewhere round them: 8-bit codes then agree bit for bit.
-__device__ __forceinline__ void update(const Step& q, float g, float& m, float& v, float& root, float& w) {
+__device__ __forceinline__ void moments(const Step& q, float g, float& m, float& v) {
   g = __fmul_rn(g, q.gscale);
   m = __fadd_rn(__fmul_rn(q.b1, m), __fmul_rn(q.one_b1, g));
   v = __fadd_rn(__fmul_rn(q.b2, v), __fmul_rn(q.one_b2, __fmul_rn(g, g)));
-  root = __fsqrt_rn(v);
-  w = w * q.keep - q.c1 * (m / (root * q.rbc2 + q.eps));
+}
+// The weight; the quotient to 2 ulp (its divisor is below 2^126).
+__device__ __forceinline__ void weight(const Step& q, float m, float root, float& w) {
+  w = w * q.keep - q.c1 * __fdividef(m, root * q.rbc2 + q.eps);
 }
 
 template <int NT, bool PBF16, bool GBF16, bool MASTER, bool BITS8>
@@ -160,6 +177,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const int step = t.vec ? 1 : 32;
     float m[8], v[8], u[8], w[8], g[8];
     const bool whole = t.vec && first + 8 <= t.n;
+    bool normal = false;                 // every v of the lane is a normal number
     if (whole) {
       const int64_t po = view_offset(t, first, t.ps);
       load8<GBF16>(t.g, view_offset(t, first, t.gs), g);
@@ -183,7 +201,23 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         load8<false>(t.v, first, v);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) update(q, g[j], m[j], v[j], u[j], w[j]);
+      for (int j = 0; j < 8; ++j) moments(q, g[j], m[j], v[j]);
+      uint32_t low = __float_as_uint(v[0]), high = low;
+#pragma unroll
+      for (int j = 1; j < 8; ++j) {
+        low = min(low, __float_as_uint(v[j]));
+        high = max(high, __float_as_uint(v[j]));
+      }
+      normal = low >= 0x00800000u && high < 0x7f800000u;
+      if (normal) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = root_normal(v[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = __fsqrt_rn(v[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) weight(q, m[j], u[j], w[j]);
       if constexpr (MASTER) store8<false>(t.w, first, w);
       store8<PBF16>(t.p, po, w);
       if constexpr (!BITS8) {
@@ -194,27 +228,29 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int64_t i = first + j * step;
-        m[j] = u[j] = 0.f;
+        m[j] = v[j] = u[j] = 0.f;
         if (i >= t.n) continue;
         const int64_t po = view_offset(t, i, t.ps);
         const float gj = load_one<GBF16>(t.g, view_offset(t, i, t.gs));
-        float vj, wj;
+        float wj;
         if constexpr (MASTER) wj = t.w[i];
         else wj = load_one<PBF16>(t.p, po);
         if constexpr (BITS8) {
           m[j] = __fmul_rn(decode2(static_cast<const uint8_t*>(t.m)[i]).x, msc);
-          vj = __fmul_rn(decode2(static_cast<const uint8_t*>(t.v)[i]).x, vsc);
-          vj = __fmul_rn(vj, vj);
+          v[j] = __fmul_rn(decode2(static_cast<const uint8_t*>(t.v)[i]).x, vsc);
+          v[j] = __fmul_rn(v[j], v[j]);
         } else {
           m[j] = static_cast<const float*>(t.m)[i];
-          vj = static_cast<const float*>(t.v)[i];
+          v[j] = static_cast<const float*>(t.v)[i];
         }
-        update(q, gj, m[j], vj, u[j], wj);
+        moments(q, gj, m[j], v[j]);
+        u[j] = __fsqrt_rn(v[j]);
+        weight(q, m[j], u[j], wj);
         if constexpr (MASTER) t.w[i] = wj;
         store_one<PBF16>(t.p, po, wj);
         if constexpr (!BITS8) {
           static_cast<float*>(t.m)[i] = m[j];
-          static_cast<float*>(t.v)[i] = vj;
+          static_cast<float*>(t.v)[i] = v[j];
         }
       }
     }
@@ -224,35 +260,50 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         mb = max(mb, __float_as_uint(m[j]) & 0x7fffffffu);
-        vb = max(vb, __float_as_uint(u[j]) & 0x7fffffffu);
+        vb = max(vb, __float_as_uint(v[j]));
       }
       float mtop = __uint_as_float(__reduce_max_sync(0xffffffffu, mb));
-      float vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, vb));
+      float vtop = __fsqrt_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, vb)));
       if (mtop < 0x1p-100f) mtop = 0.f;
       if (vtop < 0x1p-100f) vtop = 0.f;
       const float minv = mtop == 0.f ? 0.f : __fmul_rn(__frcp_rn(mtop), 448.0f);
       const float vinv = vtop == 0.f ? 0.f : __fmul_rn(__frcp_rn(vtop), 448.0f);
-      uint32_t cm[8], cv[8];
+      uint32_t wm[2], wv[2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t h = mix32((uint32_t)(first + j * step) ^ seed);
-        cm[j] = encode_abs(fabsf(m[j]), minv, h & 0xffffu);
-        if (cm[j] != 0) cm[j] |= (__float_as_uint(m[j]) >> 24) & 0x80u;
-        cv[j] = encode_abs(u[j], vinv, h >> 16);
-        if (u[j] > 0.f && vinv != 0.f && cv[j] == 0) cv[j] = 1u;
+      for (int k = 0; k < 2; ++k) {
+        uint32_t cm[4], cv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = 4 * k + i;
+          const uint32_t h = mix32((uint32_t)(first + j * step) ^ seed);
+          cm[i] = encode_top(m[j], minv, h & 0xffffu);
+          cv[i] = encode_top(u[j], vinv, h >> 16);
+        }
+        wm[k] = top_bytes(cm[0], cm[1], cm[2], cm[3]);
+        const uint32_t sign = top_bytes(__float_as_uint(m[4 * k]), __float_as_uint(m[4 * k + 1]),
+                                        __float_as_uint(m[4 * k + 2]), __float_as_uint(m[4 * k + 3]));
+        wm[k] |= sign & nonzero_bytes(wm[k]);              // (zero has no sign)
+        // a positive root is never stored as zero
+        wv[k] = top_bytes(cv[0], cv[1], cv[2], cv[3]);
+        uint32_t least = 0x01010101u;
+        if (!normal) {
+          least = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) least |= (u[4 * k + i] > 0.f ? 1u : 0u) << (8 * i);
+        }
+        if (vinv != 0.f) wv[k] |= least & ((nonzero_bytes(wv[k]) ^ 0x80808080u) >> 7);
       }
       // (the codes' memory is whole blocks: no end to look at)
       uint8_t* dm = static_cast<uint8_t*>(t.m) + first;
       uint8_t* dv = static_cast<uint8_t*>(t.v) + first;
       if (t.vec) {
-        const auto pack = [](const uint32_t* c) { return c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24; };
-        *reinterpret_cast<uint2*>(dm) = make_uint2(pack(cm), pack(cm + 4));
-        *reinterpret_cast<uint2*>(dv) = make_uint2(pack(cv), pack(cv + 4));
+        *reinterpret_cast<uint2*>(dm) = make_uint2(wm[0], wm[1]);
+        *reinterpret_cast<uint2*>(dv) = make_uint2(wv[0], wv[1]);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          dm[32 * j] = (uint8_t)cm[j];
-          dv[32 * j] = (uint8_t)cv[j];
+          dm[32 * j] = (uint8_t)(wm[j / 4] >> (8 * (j & 3)));
+          dv[32 * j] = (uint8_t)(wv[j / 4] >> (8 * (j & 3)));
         }
       }
       if (lane == 0) {
