@@ -26,7 +26,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlockElems = 256;     // elements that share a scale, and a warp's share
-constexpr int kChunk = (kThreads / 32) * kBlockElems;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxRun = 32;                            // blocks per warp and chunk: a lane holds each's scales
+constexpr int kChunk = kWarps * kBlockElems;            // elements of a chunk, times blocks per warp
 
 struct Tensor {
   void* p;
@@ -52,20 +54,60 @@ struct AdamwArgs {
   const float* grad_scale;
   long long* step;
   int advance;
+  int blocks;              // blocks of 256 elements per warp and chunk
 };
 
+// A 32-bit integer mix (xor-shifts and odd multipliers: the fractional parts of the golden
+// ratio and of the square root of 3).
+__device__ __forceinline__ uint32_t mix_end(uint32_t x) {   // from x ^ (x >> 16)
+  x *= 0x9E3779B9u;
+  return (x ^ (x >> 15)) * 0xBB67AE85u;                     // (the last x ^= x >> 16 is the caller's)
+}
 __device__ __forceinline__ uint32_t mix32(uint32_t x) {
-  x = (x ^ (x >> 16)) * 0x9E3779B9u;
-  x = (x ^ (x >> 15)) * 0xBB67AE85u;
+  x = mix_end(x ^ (x >> 16));
   return x ^ (x >> 16);
 }
 
-// e4m3 code of y = |x| inv, 0 <= y <= 448, in the low bits of the top byte: moving e4m3's
-// exponents to the bottom of fp32's (times 2^-120) makes e4m3's subnormals fp32's own, after
-// which the low 20 mantissa bits are what is rounded: up if they and 20 random bits (16 and
-// zeros) carry.
-__device__ __forceinline__ uint32_t encode_top(float x, float inv, uint32_t rnd16) {
-  return (__float_as_uint(__fmul_rn(fabsf(__fmul_rn(x, inv)), 0x1p-120f)) + rnd16 * 16u) << 4;
+// Two fp32 numbers for the packed operations (each rounded as the scalar one is), which issue
+// once for both.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max_nan_abs(float a, float b) {   // a NaN wins
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+// e4m3 code of |y|, |y| <= 448, in the top byte's low bits, from z = y 2^-120: that moves
+// e4m3's exponents to the bottom of fp32's and makes e4m3's subnormals fp32's own, after which
+// the low 20 mantissa bits are what is rounded: up if they and 20 random bits (16 and zeros)
+// carry.  The shift drops the sign.
+__device__ __forceinline__ uint32_t encode_top(float z, uint32_t rnd16) {
+  return (__float_as_uint(z) + rnd16 * 16u) << 4;
 }
 // The top bytes of four words.
 __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -74,14 +116,15 @@ __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c
 // 0x80 in every byte that is not zero (bytes up to 0x80).
 __device__ __forceinline__ uint32_t nonzero_bytes(uint32_t w) { return (w + 0x7f7f7f7fu) & 0x80808080u; }
 
-// The rounded square root of a normal v: one Newton step (v - s^2) / (2 s) from s = v rsqrt(v).
-// Equal to __fsqrt_rn for all 2^24 values of [1, 4) (and so for their scalings by 4^k), in half
-// its instructions: the 8-bit step is bound by instruction issue.
-__device__ __forceinline__ float root_normal(float v) {
+__device__ __forceinline__ float rsqrt_normal(float v) {
   float r;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  const float s = __fmul_rn(v, r);
-  return __fmaf_rn(__fmaf_rn(-s, s, v), 0.5f * r, s);
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // Two codes (the low bytes) as floats; e4m3 to fp16 and fp32 is exact.
@@ -142,13 +185,255 @@ __device__ __forceinline__ void moments(const Step& q, float g, float& m, float&
   m = __fadd_rn(__fmul_rn(q.b1, m), __fmul_rn(q.one_b1, g));
   v = __fadd_rn(__fmul_rn(q.b2, v), __fmul_rn(q.one_b2, __fmul_rn(g, g)));
 }
-// The weight; the quotient to 2 ulp (its divisor is below 2^126).
+// The weight; the quotient by an approximate reciprocal (1 ulp).
 __device__ __forceinline__ void weight(const Step& q, float m, float root, float& w) {
-  w = w * q.keep - q.c1 * __fdividef(m, root * q.rbc2 + q.eps);
+  w = w * q.keep - q.c1 * (m * rcp_approx(root * q.rbc2 + q.eps));
 }
 
+// Eight elements two at a time: m, v, sqrt(v), w from m, v, g, w.  Returns whether every v is a
+// normal number.  The root of a normal v is one Newton step (v - s^2) / (2 s) from
+// s = v rsqrt(v): equal to __fsqrt_rn for all 2^24 values of [1, 4), and so for their scalings
+// by 4^k, in half its instructions (the 8-bit step is bound by instruction issue).
+__device__ __forceinline__ bool update8(const Step& q, const float (&g)[8], float (&m)[8], float (&v)[8],
+                                        float (&u)[8], float (&w)[8]) {
+  const f32x2 b1 = pack2(q.b1, q.b1), b2 = pack2(q.b2, q.b2), o1 = pack2(q.one_b1, q.one_b1),
+              o2 = pack2(q.one_b2, q.one_b2), gs = pack2(q.gscale, q.gscale), rb = pack2(q.rbc2, q.rbc2),
+              ep = pack2(q.eps, q.eps), kp = pack2(q.keep, q.keep), nc = pack2(-q.c1, -q.c1),
+              mone = pack2(-1.f, -1.f), mhalf = pack2(-0.5f, -0.5f);
+  f32x2 M[4], V[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const f32x2 G = mul2(pack2(g[2 * j], g[2 * j + 1]), gs);
+    M[j] = add2(mul2(b1, pack2(m[2 * j], m[2 * j + 1])), mul2(o1, G));
+    V[j] = add2(mul2(b2, pack2(v[2 * j], v[2 * j + 1])), mul2(o2, mul2(G, G)));
+    const float2 x = unpack2(M[j]), y = unpack2(V[j]);
+    m[2 * j] = x.x; m[2 * j + 1] = x.y;
+    v[2 * j] = y.x; v[2 * j + 1] = y.y;
+  }
+  uint32_t low = __float_as_uint(v[0]), high = low;
+#pragma unroll
+  for (int j = 1; j < 8; ++j) {
+    low = min(low, __float_as_uint(v[j]));
+    high = max(high, __float_as_uint(v[j]));
+  }
+  const bool normal = low >= 0x00800000u && high < 0x7f800000u;
+  if (normal) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f32x2 r = pack2(rsqrt_normal(v[2 * j]), rsqrt_normal(v[2 * j + 1]));
+      const f32x2 s = mul2(V[j], r);
+      const float2 x = unpack2(fma2(fma2(s, s, mul2(V[j], mone)), mul2(r, mhalf), s));
+      u[2 * j] = x.x; u[2 * j + 1] = x.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = __fsqrt_rn(v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 den = unpack2(fma2(pack2(u[2 * j], u[2 * j + 1]), rb, ep));
+    const f32x2 t = mul2(M[j], pack2(rcp_approx(den.x), rcp_approx(den.y)));
+    const float2 x = unpack2(fma2(t, nc, mul2(pack2(w[2 * j], w[2 * j + 1]), kp)));
+    w[2 * j] = x.x; w[2 * j + 1] = x.y;
+  }
+  return normal;
+}
+
+__device__ __forceinline__ void decode_m(uint2 c, float scale, float (&m)[8]) {
+  const f32x2 s2 = pack2(scale, scale);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = decode2((j < 2 ? c.x : c.y) >> (16 * (j & 1)) & 0xffffu);
+    const float2 y = unpack2(mul2(pack2(x.x, x.y), s2));
+    m[2 * j] = y.x;
+    m[2 * j + 1] = y.y;
+  }
+}
+__device__ __forceinline__ void decode_v(uint2 c, float scale, float (&v)[8]) {
+  const f32x2 s2 = pack2(scale, scale);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = decode2((j < 2 ? c.x : c.y) >> (16 * (j & 1)) & 0xffffu);
+    const f32x2 r = mul2(pack2(x.x, x.y), s2);
+    const float2 y = unpack2(mul2(r, r));
+    v[2 * j] = y.x;
+    v[2 * j + 1] = y.y;
+  }
+}
+
+// The codes of a warp's block of 256 elements and its scales.  Lane's elements: index, index +
+// step, ...; normal: all its v are normal numbers.
+__device__ __forceinline__ void encode_block(const float (&m)[8], const float (&v)[8], const float (&u)[8],
+                                             uint32_t index, uint32_t step, uint32_t seed, bool normal,
+                                             uint2& cm, uint2& cv, float& ms, float& vs) {
+  float mt = fabsf(m[0]);
+  uint32_t vb = __float_as_uint(v[0]);
+#pragma unroll
+  for (int j = 1; j < 8; ++j) {
+    mt = max_nan_abs(mt, m[j]);
+    vb = max(vb, __float_as_uint(v[j]));
+  }
+  // non-negative floats order as their bits, a NaN above all; the root keeps the order
+  float mtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mt) & 0x7fffffffu));
+  float vtop = __fsqrt_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, vb)));
+  if (mtop < 0x1p-100f) mtop = 0.f;
+  if (vtop < 0x1p-100f) vtop = 0.f;
+  const float minv = mtop == 0.f ? 0.f : __fmul_rn(__frcp_rn(mtop), 448.0f);
+  const float vinv = vtop == 0.f ? 0.f : __fmul_rn(__frcp_rn(vtop), 448.0f);
+  ms = __fmul_rn(mtop, 1.0f / 448.0f);
+  vs = __fmul_rn(vtop, 1.0f / 448.0f);
+  const f32x2 mi = pack2(minv, minv), vi = pack2(vinv, vinv), down = pack2(0x1p-120f, 0x1p-120f);
+  // The mix of index ^ seed begins with x ^ (x >> 16).  A lane's indexes in a row differ in
+  // their low three bits only, which the shift does not reach.
+  const uint32_t x0 = index ^ seed, y0 = x0 ^ (x0 >> 16);
+  uint32_t wm[2], wv[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t tm[4], tv[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const int j = 4 * k + i;
+      const float2 zm = unpack2(mul2(mul2(pack2(m[j], m[j + 1]), mi), down));
+      const float2 zv = unpack2(mul2(mul2(pack2(u[j], u[j + 1]), vi), down));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t y = y0 ^ (uint32_t)(j + e);
+        if (step != 1) {
+          const uint32_t x = (index + (j + e) * step) ^ seed;
+          y = x ^ (x >> 16);
+        }
+        const uint32_t h = mix_end(y), hi = h >> 16;
+        tm[i + e] = encode_top(e ? zm.y : zm.x, (h ^ hi) & 0xffffu);
+        tv[i + e] = encode_top(e ? zv.y : zv.x, hi);
+      }
+    }
+    wm[k] = top_bytes(tm[0], tm[1], tm[2], tm[3]);
+    const uint32_t sign = top_bytes(__float_as_uint(m[4 * k]), __float_as_uint(m[4 * k + 1]),
+                                    __float_as_uint(m[4 * k + 2]), __float_as_uint(m[4 * k + 3]));
+    wm[k] |= sign & nonzero_bytes(wm[k]);              // (zero has no sign)
+    // a positive root is never stored as zero
+    wv[k] = top_bytes(tv[0], tv[1], tv[2], tv[3]);
+    uint32_t least = 0x01010101u;
+    if (!normal) {
+      least = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) least |= (u[4 * k + i] > 0.f ? 1u : 0u) << (8 * i);
+    }
+    if (vinv != 0.f) wv[k] |= least & ((nonzero_bytes(wv[k]) ^ 0x80808080u) >> 7);
+  }
+  cm = make_uint2(wm[0], wm[1]);
+  cv = make_uint2(wv[0], wv[1]);
+}
+
+// One warp's block of 256 elements of any tensor: 16-byte accesses where the lane's eight
+// elements lie together and are there, else element by element (every 32nd element a lane, so
+// that the warp's accesses are consecutive).
+template <bool PBF16, bool GBF16, bool MASTER, bool BITS8>
+__device__ __forceinline__ void any_block(const Tensor& t, int64_t base, const Step& q, uint32_t seed) {
+  const int lane = lane_id();
+  const int64_t blk = base / kBlockElems;
+  float msc = 0.f, vsc = 0.f;
+  if constexpr (BITS8) { msc = t.ms[blk]; vsc = t.vs[blk]; }
+  const int64_t first = t.vec ? base + 8 * lane : base + lane;
+  const int step = t.vec ? 1 : 32;
+  float m[8], v[8], u[8], w[8], g[8];
+  bool normal = false;
+  if (t.vec && first + 8 <= t.n) {
+    const int64_t po = view_offset(t, first, t.ps);
+    load8<GBF16>(t.g, view_offset(t, first, t.gs), g);
+    if constexpr (MASTER) load8<false>(t.w, first, w);
+    else load8<PBF16>(t.p, po, w);
+    if constexpr (BITS8) {
+      decode_m(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + first), msc, m);
+      decode_v(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + first), vsc, v);
+    } else {
+      load8<false>(t.m, first, m);
+      load8<false>(t.v, first, v);
+    }
+    normal = update8(q, g, m, v, u, w);
+    if constexpr (MASTER) store8<false>(t.w, first, w);
+    store8<PBF16>(t.p, po, w);
+    if constexpr (!BITS8) {
+      store8<false>(t.m, first, m);
+      store8<false>(t.v, first, v);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t i = first + j * step;
+      m[j] = v[j] = u[j] = 0.f;
+      if (i >= t.n) continue;
+      const int64_t po = view_offset(t, i, t.ps);
+      const float gj = load_one<GBF16>(t.g, view_offset(t, i, t.gs));
+      float wj;
+      if constexpr (MASTER) wj = t.w[i];
+      else wj = load_one<PBF16>(t.p, po);
+      if constexpr (BITS8) {
+        m[j] = __fmul_rn(decode2(static_cast<const uint8_t*>(t.m)[i]).x, msc);
+        v[j] = __fmul_rn(decode2(static_cast<const uint8_t*>(t.v)[i]).x, vsc);
+        v[j] = __fmul_rn(v[j], v[j]);
+      } else {
+        m[j] = static_cast<const float*>(t.m)[i];
+        v[j] = static_cast<const float*>(t.v)[i];
+      }
+      moments(q, gj, m[j], v[j]);
+      u[j] = __fsqrt_rn(v[j]);
+      weight(q, m[j], u[j], wj);
+      if constexpr (MASTER) t.w[i] = wj;
+      store_one<PBF16>(t.p, po, wj);
+      if constexpr (!BITS8) {
+        static_cast<float*>(t.m)[i] = m[j];
+        static_cast<float*>(t.v)[i] = v[j];
+      }
+    }
+  }
+  if constexpr (BITS8) {
+    uint2 cm, cv;
+    float ms, vs;
+    encode_block(m, v, u, (uint32_t)first, (uint32_t)step, seed, normal, cm, cv, ms, vs);
+    // (the codes' memory is whole blocks: no end to look at)
+    uint8_t* dm = static_cast<uint8_t*>(t.m) + first;
+    uint8_t* dv = static_cast<uint8_t*>(t.v) + first;
+    if (t.vec) {
+      *reinterpret_cast<uint2*>(dm) = cm;
+      *reinterpret_cast<uint2*>(dv) = cv;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dm[32 * j] = (uint8_t)((j < 4 ? cm.x : cm.y) >> (8 * (j & 3)));
+        dv[32 * j] = (uint8_t)((j < 4 ? cv.x : cv.y) >> (8 * (j & 3)));
+      }
+    }
+    if (lane == 0) {
+      t.ms[blk] = ms;
+      t.vs[blk] = vs;
+    }
+  }
+}
+
+// Eight consecutive elements as they lie in memory.
+template <bool BF16>
+struct Raw8 {
+  uint4 q[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* p) {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) q[i] = static_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    if constexpr (BF16) {
+      unpack8(q[0], x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[4 * i] = __uint_as_float(q[i].x); x[4 * i + 1] = __uint_as_float(q[i].y);
+        x[4 * i + 2] = __uint_as_float(q[i].z); x[4 * i + 3] = __uint_as_float(q[i].w);
+      }
+    }
+  }
+};
+
 template <int NT, bool PBF16, bool GBF16, bool MASTER, bool BITS8>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwArgs<NT> a) {
+__global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 5) adamw_kernel(const __grid_constant__ AdamwArgs<NT> a) {
   pdl_begin();
   const int lane = lane_id();
   const long long t_step = a.step[0] + 1;
@@ -158,7 +443,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   const Step q = {a.b1, a.b2, a.one_b1, a.one_b2, a.eps, a.grad_scale != nullptr ? *a.grad_scale : 1.0f,
                   lr / -expm1f(tf * a.ln_b1), 1.0f / sqrtf(-expm1f(tf * a.ln_b2)), 1.0f - lr * a.wd};
   const uint32_t seed = mix32((uint32_t)t_step);
-  const int n_chunks = a.chunk0[a.n];
+  const int n_chunks = a.chunk0[a.n], blocks = a.blocks;
   for (int c = blockIdx.x; c < n_chunks; c += gridDim.x) {
     int lo = 0, hi = a.n;                      // the chunk's tensor: chunk0[lo] <= c < chunk0[lo + 1]
     while (hi - lo > 1) {
@@ -166,151 +451,70 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       if (a.chunk0[mid] <= c) lo = mid; else hi = mid;
     }
     const Tensor& t = a.t[lo];
-    const int64_t base = (int64_t)(c - a.chunk0[lo]) * kChunk + warp_id() * kBlockElems;
-    if (base >= t.n) continue;
-    const int64_t blk = base / kBlockElems;
-    float msc = 0.f, vsc = 0.f;
-    if constexpr (BITS8) { msc = t.ms[blk]; vsc = t.vs[blk]; }
-    // lane's elements: eight in a row where 16-byte accesses are possible (first = base +
-    // 8 lane, step 1), else every 32nd (first = base + lane, step 32)
-    const int64_t first = t.vec ? base + 8 * lane : base + lane;
-    const int step = t.vec ? 1 : 32;
-    float m[8], v[8], u[8], w[8], g[8];
-    const bool whole = t.vec && first + 8 <= t.n;
-    bool normal = false;                 // every v of the lane is a normal number
-    if (whole) {
-      const int64_t po = view_offset(t, first, t.ps);
-      load8<GBF16>(t.g, view_offset(t, first, t.gs), g);
-      if constexpr (MASTER) load8<false>(t.w, first, w);
-      else load8<PBF16>(t.p, po, w);
-      if constexpr (BITS8) {
-        const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + first);
-        const uint2 cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + first);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x = decode2((j < 2 ? cm.x : cm.y) >> (16 * (j & 1)) & 0xffffu);
-          const float2 y = decode2((j < 2 ? cv.x : cv.y) >> (16 * (j & 1)) & 0xffffu);
-          m[2 * j] = __fmul_rn(x.x, msc);
-          m[2 * j + 1] = __fmul_rn(x.y, msc);
-          const float y0 = __fmul_rn(y.x, vsc), y1 = __fmul_rn(y.y, vsc);
-          v[2 * j] = __fmul_rn(y0, y0);
-          v[2 * j + 1] = __fmul_rn(y1, y1);
-        }
-      } else {
-        load8<false>(t.m, first, m);
-        load8<false>(t.v, first, v);
+    // this warp's `blocks` blocks of the chunk
+    int64_t base = ((int64_t)(c - a.chunk0[lo]) * kWarps + warp_id()) * blocks * kBlockElems;
+    int left = blocks;
+    if (BITS8 && t.vec && t.d2 == 0) {
+      const int64_t first = base + 8 * lane;
+      // whole blocks among them
+      const int64_t room = t.n - base - kBlockElems;
+      int whole = room < 0 ? 0 : room >= (int64_t)(blocks - 1) * kBlockElems ? blocks : (int)(room / kBlockElems) + 1;
+      uint8_t* pp = static_cast<uint8_t*>(t.p) + first * (PBF16 ? 2 : 4);
+      const uint8_t* pg = static_cast<const uint8_t*>(t.g) + first * (GBF16 ? 2 : 4);
+      float* pw = MASTER ? t.w + first : nullptr;
+      uint8_t* pm = static_cast<uint8_t*>(t.m) + first;
+      uint8_t* pv = static_cast<uint8_t*>(t.v) + first;
+      // lane b holds the old, and after its turn the new, scales of block b
+      const int64_t blk = base / kBlockElems + lane;
+      float lms = 0.f, lvs = 0.f;
+      if (lane < whole) {
+        lms = t.ms[blk];
+        lvs = t.vs[blk];
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) moments(q, g[j], m[j], v[j]);
-      uint32_t low = __float_as_uint(v[0]), high = low;
-#pragma unroll
-      for (int j = 1; j < 8; ++j) {
-        low = min(low, __float_as_uint(v[j]));
-        high = max(high, __float_as_uint(v[j]));
-      }
-      normal = low >= 0x00800000u && high < 0x7f800000u;
-      if (normal) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = root_normal(v[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = __fsqrt_rn(v[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) weight(q, m[j], u[j], w[j]);
-      if constexpr (MASTER) store8<false>(t.w, first, w);
-      store8<PBF16>(t.p, po, w);
-      if constexpr (!BITS8) {
-        store8<false>(t.m, first, m);
-        store8<false>(t.v, first, v);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t i = first + j * step;
-        m[j] = v[j] = u[j] = 0.f;
-        if (i >= t.n) continue;
-        const int64_t po = view_offset(t, i, t.ps);
-        const float gj = load_one<GBF16>(t.g, view_offset(t, i, t.gs));
-        float wj;
-        if constexpr (MASTER) wj = t.w[i];
-        else wj = load_one<PBF16>(t.p, po);
-        if constexpr (BITS8) {
-          m[j] = __fmul_rn(decode2(static_cast<const uint8_t*>(t.m)[i]).x, msc);
-          v[j] = __fmul_rn(decode2(static_cast<const uint8_t*>(t.v)[i]).x, vsc);
-          v[j] = __fmul_rn(v[j], v[j]);
-        } else {
-          m[j] = static_cast<const float*>(t.m)[i];
-          v[j] = static_cast<const float*>(t.v)[i];
-        }
-        moments(q, gj, m[j], v[j]);
-        u[j] = __fsqrt_rn(v[j]);
-        weight(q, m[j], u[j], wj);
-        if constexpr (MASTER) t.w[i] = wj;
-        store_one<PBF16>(t.p, po, wj);
-        if constexpr (!BITS8) {
-          static_cast<float*>(t.m)[i] = m[j];
-          static_cast<float*>(t.v)[i] = v[j];
+      Raw8<GBF16> rg;
+      Raw8<PBF16 && !MASTER> rw;
+      uint2 rm, rv;
+      const auto fetch = [&](int b) {
+        const int i = b * kBlockElems;
+        rg.load(pg + i * (GBF16 ? 2 : 4));
+        if constexpr (MASTER) rw.load(pw + i);
+        else rw.load(pp + i * (PBF16 ? 2 : 4));
+        rm = *reinterpret_cast<const uint2*>(pm + i);
+        rv = *reinterpret_cast<const uint2*>(pv + i);
+      };
+      if (whole > 0) fetch(0);
+#pragma unroll 1
+      for (int b = 0; b < whole; ++b) {
+        const int i = b * kBlockElems;
+        float m[8], v[8], u[8], w[8], g[8];
+        rg.get(g);
+        rw.get(w);
+        decode_m(rm, __shfl_sync(0xffffffffu, lms, b), m);
+        decode_v(rv, __shfl_sync(0xffffffffu, lvs, b), v);
+        // the next block's bytes are on their way while this one is computed
+        if (b + 1 < whole) fetch(b + 1);
+        const bool normal = update8(q, g, m, v, u, w);
+        if constexpr (MASTER) store8<false>(pw, i, w);
+        store8<PBF16>(pp, i, w);
+        uint2 cm, cv;
+        float ms, vs;
+        encode_block(m, v, u, (uint32_t)first + i, 1u, seed, normal, cm, cv, ms, vs);
+        *reinterpret_cast<uint2*>(pm + i) = cm;
+        *reinterpret_cast<uint2*>(pv + i) = cv;
+        if (lane == b) {
+          lms = ms;
+          lvs = vs;
         }
       }
+      if (lane < whole) {
+        t.ms[blk] = lms;
+        t.vs[blk] = lvs;
+      }
+      base += (int64_t)whole * kBlockElems;
+      left -= whole;
     }
-    if constexpr (BITS8) {
-      // non-negative floats order as their bits, a NaN above all
-      uint32_t mb = 0, vb = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        mb = max(mb, __float_as_uint(m[j]) & 0x7fffffffu);
-        vb = max(vb, __float_as_uint(v[j]));
-      }
-      float mtop = __uint_as_float(__reduce_max_sync(0xffffffffu, mb));
-      float vtop = __fsqrt_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, vb)));
-      if (mtop < 0x1p-100f) mtop = 0.f;
-      if (vtop < 0x1p-100f) vtop = 0.f;
-      const float minv = mtop == 0.f ? 0.f : __fmul_rn(__frcp_rn(mtop), 448.0f);
-      const float vinv = vtop == 0.f ? 0.f : __fmul_rn(__frcp_rn(vtop), 448.0f);
-      uint32_t wm[2], wv[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t cm[4], cv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = 4 * k + i;
-          const uint32_t h = mix32((uint32_t)(first + j * step) ^ seed);
-          cm[i] = encode_top(m[j], minv, h & 0xffffu);
-          cv[i] = encode_top(u[j], vinv, h >> 16);
-        }
-        wm[k] = top_bytes(cm[0], cm[1], cm[2], cm[3]);
-        const uint32_t sign = top_bytes(__float_as_uint(m[4 * k]), __float_as_uint(m[4 * k + 1]),
-                                        __float_as_uint(m[4 * k + 2]), __float_as_uint(m[4 * k + 3]));
-        wm[k] |= sign & nonzero_bytes(wm[k]);              // (zero has no sign)
-        // a positive root is never stored as zero
-        wv[k] = top_bytes(cv[0], cv[1], cv[2], cv[3]);
-        uint32_t least = 0x01010101u;
-        if (!normal) {
-          least = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) least |= (u[4 * k + i] > 0.f ? 1u : 0u) << (8 * i);
-        }
-        if (vinv != 0.f) wv[k] |= least & ((nonzero_bytes(wv[k]) ^ 0x80808080u) >> 7);
-      }
-      // (the codes' memory is whole blocks: no end to look at)
-      uint8_t* dm = static_cast<uint8_t*>(t.m) + first;
-      uint8_t* dv = static_cast<uint8_t*>(t.v) + first;
-      if (t.vec) {
-        *reinterpret_cast<uint2*>(dm) = make_uint2(wm[0], wm[1]);
-        *reinterpret_cast<uint2*>(dv) = make_uint2(wv[0], wv[1]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          dm[32 * j] = (uint8_t)(wm[j / 4] >> (8 * (j & 3)));
-          dv[32 * j] = (uint8_t)(wv[j / 4] >> (8 * (j & 3)));
-        }
-      }
-      if (lane == 0) {
-        t.ms[blk] = __fmul_rn(mtop, 1.0f / 448.0f);
-        t.vs[blk] = __fmul_rn(vtop, 1.0f / 448.0f);
-      }
-    }
+    for (; left > 0 && base < t.n; --left, base += kBlockElems)
+      any_block<PBF16, GBF16, MASTER, BITS8>(t, base, q, seed);
   }
   if (a.advance) {
     // every block has read the step before it arrives; the last one moves it on
@@ -325,10 +529,35 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   }
 }
 
+// Tensors per launch: a short table for few (kernel parameters are copied at every launch),
+// a long one that fills the 32764 bytes that a kernel's parameters may take.
+constexpr int kShort = 16, kLong = 240;
+static_assert(sizeof(AdamwArgs<kLong>) <= 32764, "kernel parameters");
+
 template <int NT, bool P, bool G, bool M, bool B8>
 cudaError_t launch(const moe_adamw_tensor_t* src, int n, const moe_adamw_config_t& c, const float* lr,
                    const float* gscale, int64_t* step, bool advance, cudaStream_t s) {
   AdamwArgs<NT> a;
+  // 8 bits: resident thread blocks that walk chunks of up to 32 blocks a warp, since a chunk's
+  // first block waits for its bytes (eight layers' adapters: RRR us with one block a warp, VVV us
+  // with 8, WWW us here); the length evens out the chunks per thread block.  Not longer than an
+  // average tensor, nor than keeps every SM busy.  32 bits: one block a warp and as many thread
+  // blocks as there are chunks (bound by HBM, 60 us for one layer; 66 us with longer chunks).
+  const int64_t resident = (int64_t)device_sms() * (B8 ? 3 : 64);
+  int64_t blocks = 0;
+  for (int i = 0; i < n; ++i)
+    blocks += (src[i].size[0] * src[i].size[1] * src[i].size[2] + kBlockElems - 1) / kBlockElems;
+  int64_t run = 1;
+  if (B8 && n > 0) {
+    const int64_t each = (blocks + resident * kWarps - 1) / (resident * kWarps);   // blocks per warp in all
+    const int64_t rounds = (each + kMaxRun - 1) / kMaxRun;
+    run = rounds > 0 ? (each + rounds - 1) / rounds : 1;
+    const int64_t most = blocks / (kWarps * (int64_t)n);
+    run = run < most ? run : most;
+    run = run < 1 ? 1 : run;
+  }
+  a.blocks = (int)run;
+  const int64_t per = (int64_t)kChunk * run;
   int64_t chunks = 0;
   for (int i = 0; i < n; ++i) {
     const moe_adamw_tensor_t& t = src[i];
@@ -348,7 +577,7 @@ cudaError_t launch(const moe_adamw_tensor_t* src, int n, const moe_adamw_config_
                       t.param_stride[0] % pe == 0 && t.param_stride[1] % pe == 0 &&
                       t.grad_stride[0] % ge == 0 && t.grad_stride[1] % ge == 0));
     a.chunk0[i] = (int32_t)chunks;
-    chunks += (d.n + kChunk - 1) / kChunk;
+    chunks += (d.n + per - 1) / per;
   }
   if (chunks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   a.chunk0[n] = (int32_t)chunks;
@@ -360,16 +589,10 @@ cudaError_t launch(const moe_adamw_tensor_t* src, int n, const moe_adamw_config_
   a.lr_dev = lr; a.grad_scale = gscale;
   a.step = reinterpret_cast<long long*>(step);
   a.advance = advance ? 1 : 0;
-  const int64_t cap = (int64_t)device_sms() * 64;
-  const unsigned grid = (unsigned)(chunks < 1 ? 1 : chunks < cap ? chunks : cap);
+  const unsigned grid = (unsigned)(chunks < 1 ? 1 : chunks < resident ? chunks : resident);
   ProfScope ps(K_ADAMW, s);
   return launch_pdl(adamw_kernel<NT, P, G, M, B8>, dim3(grid), dim3(kThreads), 0, s, 1, a);
 }
-
-// Tensors per launch: a short table for few (kernel parameters are copied at every launch),
-// a long one that fills the 32764 bytes that a kernel's parameters may take.
-constexpr int kShort = 16, kLong = 240;
-static_assert(sizeof(AdamwArgs<kLong>) <= 32764, "kernel parameters");
 
 template <bool P, bool G, bool M, bool B8>
 cudaError_t launch_all(const moe_adamw_tensor_t* src, int n, const moe_adamw_config_t& c, const float* lr,
