@@ -539,10 +539,11 @@ cudaError_t launch(const moe_adamw_tensor_t* src, int n, const moe_adamw_config_
                    const float* gscale, int64_t* step, bool advance, cudaStream_t s) {
   AdamwArgs<NT> a;
   // 8 bits: resident thread blocks that walk chunks of up to 32 blocks a warp, since a chunk's
-  // first block waits for its bytes (eight layers' adapters: RRR us with one block a warp, VVV us
-  // with 8, WWW us here); the length evens out the chunks per thread block.  Not longer than an
+  // first block waits for its bytes (eight layers' adapters: 253 us with 8 blocks a warp, 238
+  // with 16, 232 with 32); the length evens out the chunks per thread block.  Not longer than an
   // average tensor, nor than keeps every SM busy.  32 bits: one block a warp and as many thread
-  // blocks as there are chunks (bound by HBM, 60 us for one layer; 66 us with longer chunks).
+  // blocks as there are chunks (bound by HBM: 60 us for one layer with master weights, 94% of
+  // the measured copy bandwidth; 66 us as a loop over longer chunks).
   const int64_t resident = (int64_t)device_sms() * (B8 ? 3 : 64);
   int64_t blocks = 0;
   for (int i = 0; i < n; ++i)
