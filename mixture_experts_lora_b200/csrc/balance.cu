@@ -8,11 +8,14 @@
 //   g_s          = dloss[s] E / (k n_s^2)
 //
 // Both directions read every logit once and are bound by HBM (the backward writes as much).
-// Forward: a block per window of rows, a warp per row (softmax in registers, lane l holds
-// experts l, l + 32, ...); the lanes sum their experts' probabilities over the warp's rows,
-// the block's warps are summed in a fixed order through shared memory, and each
-// (window, sequence) pair writes one partial row; a second launch sums a sequence's
-// partials in window order.  Everything is fp32 (counts: integers).
+// Rows are cut into windows, a block each.  A row is spread over L lanes (a power of two, 32
+// from 128 experts on: fewer lanes leave room for several rows in a warp), each holding NQ
+// groups of V experts, V = 4 where rows are 16-byte aligned.  A warp loads U rows per lane
+// group before it works on the first, so that enough bytes are on their way.
+// Forward: the lanes sum their experts' probabilities over the rows, the block's warps are
+// summed in a fixed order through shared memory, and each (window, sequence) pair writes one
+// partial row; a second launch sums a sequence's partials in window order.  A batch of one
+// window needs no second launch.  Everything is fp32 (counts: integers).
 #include "common.cuh"
 #include "internal.h"
 #include "sequences.cuh"
@@ -32,9 +35,14 @@ struct BalanceArgs {
   int E, k, S;
   int rows;                // rows per window
   // forward: partial rows of the (window, sequence) slots
+  // partials, or (one window) the outputs themselves
   float* psum;             // [slots][E]
   int32_t* pcnt;           // [slots][E]
   int32_t* pn;             // [slots]
+  float* loss;             // outputs; balance_partial_kernel writes them itself if loss is set
+  int32_t* out_counts;
+  int32_t* out_n;
+  int lanes;               // lanes per row
   int* err;
   // backward
   const int32_t* counts;
@@ -44,110 +52,233 @@ struct BalanceArgs {
   int accumulate;
 };
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// The row's softmax, lane l's experts l + 32 q in p[q] (0 past E; all 0 for a row of -inf).
-template <int PL>
-__device__ __forceinline__ void row_softmax(const float* __restrict__ x, int E, int lane,
-                                            float (&p)[PL]) {
-  float mx = -INFINITY;
-#pragma unroll
-  for (int q = 0; q < PL; ++q) {
-    const int e = lane + 32 * q;
-    p[q] = e < E ? x[e] : -INFINITY;
-    mx = fmaxf(mx, p[q]);
+// How a row lies in a warp: V consecutive experts at a time, NQ times; FULL: over all 32 lanes.
+template <int V_, int NQ_, bool FULL_>
+struct RowCfg {
+  static constexpr int V = V_, NQ = NQ_, N = V * NQ;
+  static constexpr bool FULL = FULL_;
+  static constexpr int U = N <= 4 ? 4 : N <= 8 ? 2 : 1;      // rows loaded at once
+};
+
+// The lanes of a row.
+struct Lanes {
+  int L, sub, group, groups;     // lanes per row, lane within its row, row within the warp, rows
+  __device__ __forceinline__ Lanes(bool full, int l) : L(full ? 32 : l) {
+    sub = lane_id() & (L - 1);
+    groups = 32 / L;
+    group = lane_id() / L;
   }
-  mx = warp_max(mx);
-  float sum = 0.f;
-#pragma unroll
-  for (int q = 0; q < PL; ++q) {
-    p[q] = p[q] == -INFINITY ? 0.f : expf(p[q] - mx);
-    sum += p[q];
+};
+template <class C>
+__device__ __forceinline__ float row_max(float v, const Lanes& ln) {
+  if constexpr (C::FULL) {
+    float r;                     // (a NaN loses)
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  } else {
+    for (int o = ln.L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
   }
-  sum = warp_sum(sum);
-  // (a NaN logit may lose the maximum's comparison; the sum carries it)
-  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-#pragma unroll
-  for (int q = 0; q < PL; ++q) p[q] *= inv;
+}
+template <class C>
+__device__ __forceinline__ float row_sum(float v, const Lanes& ln) {
+  if constexpr (C::FULL) return warp_sum(v);
+  for (int o = ln.L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
-template <int PL>
+// First expert of the lane's group q.
+template <class C>
+__device__ __forceinline__ int expert_of(const Lanes& ln, int q) { return (q * ln.L + ln.sub) * C::V; }
+
+// The lane's experts of a row (px: the row's first of them), -inf past E and where !live.
+template <class C>
+__device__ __forceinline__ void load_row(const float* __restrict__ px, int E, const Lanes& ln, bool live,
+                                         float (&v)[C::N]) {
+#pragma unroll
+  for (int q = 0; q < C::NQ; ++q) {
+    const bool in = live && expert_of<C>(ln, q) < E;
+    if constexpr (C::V == 4) {
+      const float4 t = in ? __ldg(reinterpret_cast<const float4*>(px + q * ln.L * 4))
+                          : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      v[4 * q] = t.x; v[4 * q + 1] = t.y; v[4 * q + 2] = t.z; v[4 * q + 3] = t.w;
+    } else {
+      v[q] = in ? __ldg(px + q * ln.L) : -INFINITY;
+    }
+  }
+}
+
+// exp(x - max) in place, 0 for -inf.  2^y to 2 ulp with y = (x - max) log2(e) rounded: a term is
+// off by |x - max| u and a few u more, u = 2^-24 (the kernel is bound by instruction issue, and
+// an exponential good to the last bit costs four times as many).
+template <class C>
+__device__ __forceinline__ void row_exp(float (&v)[C::N], const Lanes& ln) {
+  float mx = v[0];
+#pragma unroll
+  for (int i = 1; i < C::N; ++i) mx = fmaxf(mx, v[i]);
+  mx = row_max<C>(mx, ln);
+  if (mx == -INFINITY) mx = 0.f;          // nothing finite: every term 2^-inf = 0
+  const f32x2 nm = pack2(-mx, -mx), l2e = pack2(1.4426950408889634f, 1.4426950408889634f);
+#pragma unroll
+  for (int i = 0; i < C::N; i += 2) {
+    const bool two = i + 1 < C::N;
+    const float2 y = unpack2(mul2(add2(pack2(v[i], two ? v[i + 1] : 0.f), nm), l2e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"(y.x));
+    if (two) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i + 1]) : "f"(y.y));
+  }
+}
+template <class C>
+__device__ __forceinline__ float lane_sum(const float (&v)[C::N]) {
+  float sum = v[0];
+#pragma unroll
+  for (int i = 1; i < C::N; ++i) sum += v[i];
+  return sum;
+}
+// 1 / (a row's sum of exponentials: at least 1, 0 or not a number), 0 for 0
+__device__ __forceinline__ float row_inverse(float sum) { return sum == 0.f ? 0.f : rcp_approx(sum); }
+
+__device__ __forceinline__ float loss_factor(int E, int k, int n) {
+  return n > 0 ? (float)E / ((float)k * (float)n) / (float)n : 0.f;
+}
+
+// The sum of one float per thread over the block (any multiple of 32 threads), in thread 0.
+__device__ __forceinline__ float block_sum(float v, float* s_part) {
+  v = warp_sum(v);
+  __syncthreads();
+  if (lane_id() == 0) s_part[warp_id()] = v;
+  __syncthreads();
+  float all = 0.f;
+  if (threadIdx.x == 0)
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) all += s_part[i];
+  return all;
+}
+
+template <class C>
 __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const BalanceArgs a) {
   pdl_begin();
   extern __shared__ float s_dyn[];            // [kWarps][E] sums, then E counts
   float* s_sum = s_dyn;
   int* s_cnt = reinterpret_cast<int*>(s_dyn + kWarps * a.E);
   __shared__ int s_n;
-  const int warp = warp_id(), lane = lane_id(), E = a.E;
+  __shared__ float s_part[kWarps];
+  const int warp = warp_id(), E = a.E;
+  const Lanes ln(C::FULL, a.lanes);
   const int64_t w = blockIdx.x, t0 = w * a.rows;
   const int64_t t1 = t0 + a.rows < a.T ? t0 + a.rows : a.T;
   int s = 0;
   if (a.off != nullptr) {
     check_offsets(a.off, a.S, a.T, a.err);
-    s = block_count_le(a.S, t0, [&](int i) { return a.off[i + 1]; });
+    // (one window: every sequence's outputs are written here, the empty ones' too)
+    if (a.loss == nullptr) s = block_count_le(a.S, t0, [&](int i) { return a.off[i + 1]; });
   }
   for (; s < a.S; ++s) {
     int64_t r0 = a.off != nullptr ? a.off[s] : 0, r1 = a.off != nullptr ? a.off[s + 1] : a.T;
-    if (r0 >= t1) break;
+    if (a.loss == nullptr && r0 >= t1) break;
     r0 = r0 > t0 ? r0 : t0;
     r1 = r1 < t1 ? r1 : t1;
-    if (r0 >= r1) continue;
+    if (a.loss == nullptr && r0 >= r1) continue;
     for (int e = threadIdx.x; e < E; e += kThreads) s_cnt[e] = 0;
     if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
-    float acc[PL];
+    // pairs per expert
+    for (int64_t i = r0 * a.k + threadIdx.x; i < r1 * a.k; i += kThreads) {
+      if (a.mask != nullptr && a.mask[(uint32_t)i / (uint32_t)a.k] == 0) continue;
+      const int e = a.ids[i];
+      if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
+      else report_error(a.err, MOE_ERR_DEVICE_INDEX);
+    }
+    float acc[C::N];
 #pragma unroll
-    for (int q = 0; q < PL; ++q) acc[q] = 0.f;
+    for (int i = 0; i < C::N; ++i) acc[i] = 0.f;
     int n = 0;
-    for (int64_t t = r0 + warp; t < r1; t += kWarps) {
-      if (a.mask != nullptr && a.mask[t] == 0) continue;
-      ++n;
-      float p[PL];
-      row_softmax<PL>(a.logits + t * E, E, lane, p);
+    const int per = ln.groups * C::U;          // rows of a warp at a time
+    const int rows = (int)(r1 - r0);
+    const int64_t skip = (int64_t)kWarps * per * E;
+    int t = warp * per + ln.group;             // the lane group's first row, from r0
+    const float* px = a.logits + (r0 + t) * E + ln.sub * C::V;
+    const uint8_t* pmask = a.mask != nullptr ? a.mask + r0 : nullptr;
+    for (int tw = warp * per; tw < rows; tw += kWarps * per, t += kWarps * per, px += skip) {
+      float v[C::U][C::N];
+      bool live[C::U];
 #pragma unroll
-      for (int q = 0; q < PL; ++q) acc[q] += p[q];
-      if (lane < a.k) {
-        const int e = a.ids[t * a.k + lane];
-        if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
-        else report_error(a.err, MOE_ERR_DEVICE_INDEX);
+      for (int u = 0; u < C::U; ++u) {
+        live[u] = t + u * ln.groups < rows && (pmask == nullptr || pmask[t + u * ln.groups] != 0);
+        load_row<C>(px + u * ln.groups * E, E, ln, live[u], v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < C::U; ++u) {
+        row_exp<C>(v[u], ln);
+        const float inv = row_inverse(row_sum<C>(lane_sum<C>(v[u]), ln));
+        n += live[u];
+#pragma unroll
+        for (int i = 0; i < C::N; ++i) acc[i] += v[u][i] * inv;
       }
     }
+    // rows of one warp side by side: the lanes of the same experts
+    if constexpr (!C::FULL) {
+      for (int o = ln.L; o < 32; o <<= 1) {
 #pragma unroll
-    for (int q = 0; q < PL; ++q)
-      if (lane + 32 * q < E) s_sum[warp * E + lane + 32 * q] = acc[q];
-    if (lane == 0) atomicAdd(&s_n, n);
+        for (int i = 0; i < C::N; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+      }
+    }
+    if (C::FULL || ln.group == 0) {
+#pragma unroll
+      for (int q = 0; q < C::NQ; ++q) {
+        const int e = expert_of<C>(ln, q);
+#pragma unroll
+        for (int i = 0; i < C::V; ++i)
+          if (e + i < E) s_sum[warp * E + e + i] = acc[q * C::V + i];
+      }
+    }
+    if (ln.sub == 0 && n > 0) atomicAdd(&s_n, n);
     __syncthreads();
     const int64_t slot = w + s;
+    float part = 0.f;
     for (int e = threadIdx.x; e < E; e += kThreads) {
       float v = 0.f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) v += s_sum[i * E + e];
-      a.psum[slot * E + e] = v;
-      a.pcnt[slot * E + e] = s_cnt[e];
+      const int cnt = s_cnt[e];
+      if (a.loss != nullptr) {
+        a.out_counts[(int64_t)s * E + e] = cnt;
+        part += (float)cnt * v;
+      } else {
+        a.psum[slot * E + e] = v;
+        a.pcnt[slot * E + e] = cnt;
+      }
     }
-    if (threadIdx.x == 0) a.pn[slot] = s_n;
+    if (a.loss != nullptr) {
+      const float all = block_sum(part, s_part);
+      if (threadIdx.x == 0) {
+        a.loss[s] = all * loss_factor(E, a.k, s_n);
+        a.out_n[s] = s_n;
+      }
+    } else if (threadIdx.x == 0) {
+      a.pn[slot] = s_n;
+    }
     __syncthreads();
   }
 }
 
-// One block per sequence: its partial rows summed in window order.
-__global__ void __launch_bounds__(kThreads)
-    balance_sum_kernel(const BalanceArgs a, float* __restrict__ loss, int32_t* __restrict__ counts,
-                       int32_t* __restrict__ n_tokens) {
+// One block per sequence: its partial rows summed in window order (a warp every warps-th
+// window, then the warps in order).
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceArgs a) {
+  const int warps = (int)blockDim.x / 32;
   pdl_begin();
-  __shared__ float s_part[kWarps];
-  const int s = blockIdx.x, E = a.E;
+  __shared__ float s_sum[32][128];
+  __shared__ int s_cnt[32][128];
+  __shared__ float s_part[32];
+  __shared__ int s_n;
+  const int s = blockIdx.x, E = a.E, warp = warp_id(), lane = lane_id();
   const int64_t n_win = (a.T + a.rows - 1) / a.rows;
-  int64_t r0 = a.off != nullptr ? a.off[s] : 0, r1 = a.off != nullptr ? a.off[s + 1] : a.T;
+  const int64_t r0 = a.off != nullptr ? a.off[s] : 0, r1 = a.off != nullptr ? a.off[s + 1] : a.T;
   // first and last window of the sequence (none if it is empty), within the table whatever
   // the offsets hold
   int64_t w0 = 0, w1 = 0;
@@ -156,36 +287,57 @@ __global__ void __launch_bounds__(kThreads)
     w1 = (r1 - 1) / a.rows + 1;
     if (w1 > n_win) w1 = n_win;
   }
-  int n = 0;
-  for (int64_t w = w0; w < w1; ++w) n += a.pn[w + s];
-  float part = 0.f;
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    float sum = 0.f;
-    int cnt = 0;
-    for (int64_t w = w0; w < w1; ++w) {
-      sum += a.psum[(w + s) * E + e];
-      cnt += a.pcnt[(w + s) * E + e];
-    }
-    counts[(int64_t)s * E + e] = cnt;
-    part += (float)cnt * sum;
-  }
-  part = warp_sum(part);
-  if (lane_id() == 0) s_part[warp_id()] = part;
+  if (threadIdx.x == 0) s_n = 0;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float all = 0.f;
+  int n = 0;
+  for (int64_t w = w0 + threadIdx.x; w < w1; w += blockDim.x) n += a.pn[w + s];
+  if (n != 0) atomicAdd(&s_n, n);
+  float part = 0.f;
+  for (int e0 = 0; e0 < E; e0 += 128) {
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    int cnt[4] = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int64_t w = w0 + warp; w < w1; w += warps) {
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) all += s_part[i];
-    const float fn = (float)n;
-    loss[s] = n > 0 ? all * ((float)E / ((float)a.k * fn)) / fn : 0.f;
-    n_tokens[s] = n;
+      for (int i = 0; i < 4; ++i) {
+        const int e = e0 + i * 32 + lane;
+        if (e < E) {
+          sum[i] += a.psum[(w + s) * E + e];
+          cnt[i] += a.pcnt[(w + s) * E + e];
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s_sum[warp][i * 32 + lane] = sum[i];
+      s_cnt[warp][i * 32 + lane] = cnt[i];
+    }
+    __syncthreads();
+    const int e = e0 + threadIdx.x;
+    if (threadIdx.x < 128 && e < E) {
+      float v = 0.f;
+      int c = 0;
+      for (int i = 0; i < warps; ++i) {
+        v += s_sum[i][threadIdx.x];
+        c += s_cnt[i][threadIdx.x];
+      }
+      a.out_counts[(int64_t)s * E + e] = c;
+      part += (float)c * v;
+    }
+  }
+  const float all = block_sum(part, s_part);
+  if (threadIdx.x == 0) {
+    a.loss[s] = all * loss_factor(E, a.k, s_n);
+    a.out_n[s] = s_n;
   }
 }
 
-template <int PL>
+template <class C>
 __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const BalanceArgs a) {
   pdl_begin();
-  const int warp = warp_id(), lane = lane_id(), E = a.E;
+  const int warp = warp_id(), E = a.E;
+  const Lanes ln(C::FULL, a.lanes);
   const int64_t t0 = (int64_t)blockIdx.x * a.rows;
   const int64_t t1 = t0 + a.rows < a.T ? t0 + a.rows : a.T;
   int s = 0;
@@ -193,57 +345,136 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
     check_offsets(a.off, a.S, a.T, a.err);
     s = block_count_le(a.S, t0, [&](int i) { return a.off[i + 1]; });
   }
-  for (int64_t t = t0 + warp; t < t1; t += kWarps) {
-    bool live = a.mask == nullptr || a.mask[t] != 0;
-    if (a.off != nullptr) {
-      while (s < a.S && a.off[s + 1] <= t) ++s;
-      live = live && s < a.S && a.off[s] <= t;
-    }
-    float* out = a.dlogits + t * E;
-    if (!live) {
-      if (!a.accumulate)
-        for (int e = lane; e < E; e += 32) out[e] = 0.f;
-      continue;
-    }
-    float p[PL], f[PL];
-    row_softmax<PL>(a.logits + t * E, E, lane, p);
-    const float n = (float)a.n_tokens[s];
-    const float g = n > 0.f ? a.dloss[s] * ((float)E / ((float)a.k * n)) / n : 0.f;
-    float dot = 0.f;
+  // everything from t0 on: rows of the window, and of the lane group's sequence s
+  const int rows = (int)(t1 - t0);
+  int s_lo = 0, s_hi = a.off != nullptr ? -1 : rows;
+  int held = -1;                               // the sequence whose f is held
+  float f[C::N];
+  const int per = ln.groups * C::U;
+  const int64_t skip = (int64_t)kWarps * per * E;
+  int t = warp * per + ln.group;
+  const int64_t first = (t0 + t) * E + ln.sub * C::V;
+  const float* px = a.logits + first;
+  float* po = a.dlogits + first;
+  const uint8_t* pmask = a.mask != nullptr ? a.mask + t0 : nullptr;
+  for (int tw = warp * per; tw < rows; tw += kWarps * per, t += kWarps * per, px += skip, po += skip) {
+    float v[C::U][C::N];
+    bool live[C::U];
+    int seq[C::U];
 #pragma unroll
-    for (int q = 0; q < PL; ++q) {
-      const int e = lane + 32 * q;
-      f[q] = e < E ? (float)a.counts[(int64_t)s * E + e] * g : 0.f;
-      dot += p[q] * f[q];
+    for (int u = 0; u < C::U; ++u) {
+      const int tu = t + u * ln.groups;
+      live[u] = tu < rows && (pmask == nullptr || pmask[tu] != 0);
+      if (tu < rows && tu >= s_hi) {           // on to the row's sequence
+        while (s < a.S && a.off[s + 1] <= t0 + tu) ++s;
+        s_lo = s < a.S ? (int)(a.off[s] - t0) : rows;
+        s_hi = s < a.S ? (int)(a.off[s + 1] - t0) : rows;
+      }
+      live[u] = live[u] && tu >= s_lo;
+      seq[u] = s;
+      load_row<C>(px + u * ln.groups * E, E, ln, live[u], v[u]);
     }
-    dot = warp_sum(dot);
 #pragma unroll
-    for (int q = 0; q < PL; ++q) {
-      const int e = lane + 32 * q;
-      if (e >= E) continue;
-      const float d = p[q] * (f[q] - dot);
-      out[e] = a.accumulate ? out[e] + d : d;
+    for (int u = 0; u < C::U; ++u) {
+      if (live[u] && seq[u] != held) {
+        held = seq[u];
+        const int n = a.n_tokens[held];
+        const float g = a.dloss[held] * loss_factor(E, a.k, n);
+        // counts less their mean: sum_j p_j = 1 lets any constant be taken off the counts, and
+        // small differences keep the digits that counts - sum_j p_j counts_j would cancel
+        const float mean = (float)a.k * (float)n / (float)E;
+#pragma unroll
+        for (int q = 0; q < C::NQ; ++q) {
+          const int e = expert_of<C>(ln, q);
+#pragma unroll
+          for (int i = 0; i < C::V; ++i)
+            f[q * C::V + i] = e + i < E ? ((float)a.counts[(int64_t)held * E + e + i] - mean) * g : 0.f;
+        }
+      }
+      row_exp<C>(v[u], ln);
+      float dot = 0.f;
+      if (live[u]) {
+#pragma unroll
+        for (int i = 0; i < C::N; ++i) dot += v[u][i] * f[i];
+      }
+      const float inv = row_inverse(row_sum<C>(lane_sum<C>(v[u]), ln));
+      dot = row_sum<C>(dot, ln) * inv;
+      if (t + u * ln.groups >= rows || (!live[u] && a.accumulate)) continue;
+      float* out = po + u * ln.groups * E;
+#pragma unroll
+      for (int q = 0; q < C::NQ; ++q) {
+        if (expert_of<C>(ln, q) >= E) continue;
+        float d[C::V];
+#pragma unroll
+        for (int i = 0; i < C::V; ++i)
+          d[i] = live[u] ? v[u][q * C::V + i] * inv * (f[q * C::V + i] - dot) : 0.f;
+        if constexpr (C::V == 4) {
+          float4* p = reinterpret_cast<float4*>(out + q * ln.L * 4);
+          float4 o = make_float4(d[0], d[1], d[2], d[3]);
+          if (a.accumulate) {
+            const float4 b = *p;
+            o = make_float4(b.x + o.x, b.y + o.y, b.z + o.z, b.w + o.w);
+          }
+          *p = o;
+        } else {
+          float* p = out + q * ln.L;
+          *p = a.accumulate ? *p + d[0] : d[0];
+        }
+      }
     }
   }
 }
 
-template <int PL>
-cudaError_t launch_forward(const BalanceArgs& a, int64_t n_win, cudaStream_t st) {
-  ProfScope ps(K_BALANCE, st);
-  return launch_pdl(balance_partial_kernel<PL>, dim3((unsigned)n_win), dim3(kThreads),
-                    (size_t)(kWarps + 1) * a.E * 4, st, 1, a);
-}
-template <int PL>
-cudaError_t launch_backward(const BalanceArgs& a, int64_t n_win, cudaStream_t st) {
-  ProfScope ps(K_BALANCE_BWD, st);
-  return launch_pdl(balance_backward_kernel<PL>, dim3((unsigned)n_win), dim3(kThreads), 0, st, 1, a);
+struct Forward {
+  template <class C>
+  static cudaError_t launch(const BalanceArgs& a, int64_t n_win, cudaStream_t st) {
+    ProfScope ps(K_BALANCE, st);
+    return launch_pdl(balance_partial_kernel<C>, dim3((unsigned)n_win), dim3(kThreads),
+                      (size_t)(kWarps + 1) * a.E * 4, st, 1, a);
+  }
+};
+struct Backward {
+  template <class C>
+  static cudaError_t launch(const BalanceArgs& a, int64_t n_win, cudaStream_t st) {
+    ProfScope ps(K_BALANCE_BWD, st);
+    return launch_pdl(balance_backward_kernel<C>, dim3((unsigned)n_win), dim3(kThreads), 0, st, 1, a);
+  }
+};
+
+// Four experts at a time where every row of logits (and of the gradient) is 16-byte aligned.
+template <class K>
+cudaError_t launch_rows(BalanceArgs& a, int64_t n_win, cudaStream_t s) {
+  const bool v4 = a.E % 4 == 0 && aligned16(a.logits) && (a.dlogits == nullptr || aligned16(a.dlogits));
+  const int groups = v4 ? a.E / 4 : a.E;
+  a.lanes = 1;
+  while (a.lanes < 32 && a.lanes < groups) a.lanes *= 2;
+  const int nq = (groups + a.lanes - 1) / a.lanes;
+  if (v4) {
+    if (a.lanes < 32) return K::template launch<RowCfg<4, 1, false>>(a, n_win, s);
+    if (nq <= 1) return K::template launch<RowCfg<4, 1, true>>(a, n_win, s);
+    if (nq <= 2) return K::template launch<RowCfg<4, 2, true>>(a, n_win, s);
+    if (nq <= 4) return K::template launch<RowCfg<4, 4, true>>(a, n_win, s);
+    return K::template launch<RowCfg<4, 8, true>>(a, n_win, s);
+  }
+  if (a.lanes < 32) return K::template launch<RowCfg<1, 1, false>>(a, n_win, s);
+  if (nq <= 1) return K::template launch<RowCfg<1, 1, true>>(a, n_win, s);
+  if (nq <= 2) return K::template launch<RowCfg<1, 2, true>>(a, n_win, s);
+  if (nq <= 4) return K::template launch<RowCfg<1, 4, true>>(a, n_win, s);
+  if (nq <= 8) return K::template launch<RowCfg<1, 8, true>>(a, n_win, s);
+  if (nq <= 16) return K::template launch<RowCfg<1, 16, true>>(a, n_win, s);
+  return K::template launch<RowCfg<1, 32, true>>(a, n_win, s);
 }
 
-// Rows per window: at most about two windows per SM, so that a sequence's partial rows stay
-// few, and at least four rows per warp.
-int window_rows(int64_t T) {
-  const int64_t per = (T + 295) / 296;
-  return (int)(per < 32 ? 32 : per);
+// Rows per window.  Batches of up to 32768 logits in few sequences: one window, which needs no
+// second launch.  Otherwise at most about four windows per SM, so that a sequence's partial rows
+// stay few, and 32 rows at least, less where sequences are shorter (a window works through its
+// sequences one after the other).
+int window_rows(int64_t T, int E, int S) {
+  if (T * E <= 32768 && S <= 4) return T > 0 ? (int)T : 1;
+  int64_t low = T / S;
+  low = low > 32 ? 32 : low < 8 ? 8 : low;
+  const int64_t per = (T + 591) / 592;
+  return (int)(per < low ? low : per);
 }
 
 moe_status_t check_shape(int64_t T, int32_t E, int32_t k, const int32_t* off, int32_t S) {
@@ -260,7 +491,7 @@ struct BalanceLayout {
 };
 BalanceLayout make_layout(int64_t T, int E, int S) {
   BalanceLayout L{};
-  const int rows = window_rows(T);
+  const int rows = window_rows(T, E, S);
   L.n_win = (T + rows - 1) / rows;
   L.slots = L.n_win + S;
   const size_t row = ((size_t)L.slots * E * 4 + 255) & ~size_t(255);
@@ -275,11 +506,6 @@ BalanceLayout make_layout(int64_t T, int E, int S) {
 }  // namespace moe
 
 using namespace moe;
-
-#define MOE_BY_EXPERTS(E, CALL)                 \
-  ((E) <= 32 ? CALL<1> : (E) <= 64 ? CALL<2>    \
-   : (E) <= 128 ? CALL<4> : (E) <= 256 ? CALL<8> \
-   : (E) <= 512 ? CALL<16> : CALL<32>)
 
 extern "C" {
 
@@ -308,7 +534,7 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_ids, int6
   a.E = E;
   a.k = k;
   a.S = S;
-  a.rows = window_rows(T);
+  a.rows = window_rows(T, E, S);
   char* base = static_cast<char*>(ws);
   a.psum = reinterpret_cast<float*>(base + L.psum);
   a.pcnt = reinterpret_cast<int32_t*>(base + L.pcnt);
@@ -316,11 +542,16 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_ids, int6
   a.err = moe_status_word();
   if (a.err == nullptr) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T > 0 && MOE_BY_EXPERTS(E, launch_forward)(a, L.n_win, s) != cudaSuccess) return MOE_ERR_CUDA;
-  {
+  a.out_counts = counts;
+  a.out_n = n_tokens;
+  const bool one = L.n_win == 1;
+  a.loss = one ? loss : nullptr;
+  if (T > 0 && launch_rows<Forward>(a, L.n_win, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (!one) {
+    a.loss = loss;
     ProfScope ps(K_BALANCE_SUM, s);
-    if (launch_pdl(balance_sum_kernel, dim3((unsigned)S), dim3(kThreads), 0, s, 1, a, loss, counts,
-                   n_tokens) != cudaSuccess)
+    if (launch_pdl(balance_sum_kernel, dim3((unsigned)S),
+                   dim3(L.n_win > 32 * (int64_t)S ? kSumThreads : kThreads), 0, s, 1, a) != cudaSuccess)
       return MOE_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -345,7 +576,7 @@ moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* count
   a.E = E;
   a.k = k;
   a.S = S;
-  a.rows = window_rows(T);
+  a.rows = window_rows(T, E, S);
   a.counts = counts;
   a.n_tokens = n_tokens;
   a.dloss = dloss;
@@ -354,7 +585,7 @@ moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* count
   a.err = moe_status_word();
   if (a.err == nullptr) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (MOE_BY_EXPERTS(E, launch_backward)(a, (T + a.rows - 1) / a.rows, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (launch_rows<Backward>(a, (T + a.rows - 1) / a.rows, s) != cudaSuccess) return MOE_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
