@@ -160,7 +160,7 @@ __device__ __forceinline__ float block_sum(float v, float* s_part) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(kThreads) balance_partial_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kThreads, C::N <= 8 ? 4 : 2) balance_partial_kernel(const BalanceArgs a) {
   pdl_begin();
   extern __shared__ float s_dyn[];            // [kWarps][E] sums, then E counts
   float* s_sum = s_dyn;
@@ -186,6 +186,30 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const Balance
     for (int e = threadIdx.x; e < E; e += kThreads) s_cnt[e] = 0;
     if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
+    float acc[C::N];
+#pragma unroll
+    for (int i = 0; i < C::N; ++i) acc[i] = 0.f;
+    int n = 0;
+    const int per = ln.groups * C::U;          // rows of a warp at a time
+    const int rows = (int)(r1 - r0), step = kWarps * per;
+    int t = warp * per + ln.group;             // the lane group's first row, from r0
+    const float* px = a.logits + (r0 + t) * E + ln.sub * C::V;
+    const uint8_t* pmask = a.mask != nullptr ? a.mask + r0 : nullptr;
+    // the next rows' logits are on their way while a row's softmax is computed
+    float next[C::U][C::N];
+    uint32_t next_live = 0;
+    const auto fetch = [&]() {
+      next_live = 0;
+#pragma unroll
+      for (int u = 0; u < C::U; ++u) {
+        const bool live = t + u * ln.groups < rows && (pmask == nullptr || pmask[t + u * ln.groups] != 0);
+        next_live |= (uint32_t)live << u;
+        load_row<C>(px + u * ln.groups * E, E, ln, live, next[u]);
+      }
+      t += step;
+      px += (int64_t)step * E;
+    };
+    fetch();
     // pairs per expert
     for (int64_t i = r0 * a.k + threadIdx.x; i < r1 * a.k; i += kThreads) {
       if (a.mask != nullptr && a.mask[(uint32_t)i / (uint32_t)a.k] == 0) continue;
@@ -193,29 +217,18 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const Balance
       if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
       else report_error(a.err, MOE_ERR_DEVICE_INDEX);
     }
-    float acc[C::N];
-#pragma unroll
-    for (int i = 0; i < C::N; ++i) acc[i] = 0.f;
-    int n = 0;
-    const int per = ln.groups * C::U;          // rows of a warp at a time
-    const int rows = (int)(r1 - r0);
-    const int64_t skip = (int64_t)kWarps * per * E;
-    int t = warp * per + ln.group;             // the lane group's first row, from r0
-    const float* px = a.logits + (r0 + t) * E + ln.sub * C::V;
-    const uint8_t* pmask = a.mask != nullptr ? a.mask + r0 : nullptr;
-    for (int tw = warp * per; tw < rows; tw += kWarps * per, t += kWarps * per, px += skip) {
+    for (int tw = warp * per; tw < rows; tw += step) {
       float v[C::U][C::N];
-      bool live[C::U];
 #pragma unroll
-      for (int u = 0; u < C::U; ++u) {
-        live[u] = t + u * ln.groups < rows && (pmask == nullptr || pmask[t + u * ln.groups] != 0);
-        load_row<C>(px + u * ln.groups * E, E, ln, live[u], v[u]);
-      }
+      for (int u = 0; u < C::U; ++u)
+#pragma unroll
+        for (int i = 0; i < C::N; ++i) v[u][i] = next[u][i];
+      n += __popc(next_live);
+      fetch();
 #pragma unroll
       for (int u = 0; u < C::U; ++u) {
         row_exp<C>(v[u], ln);
         const float inv = row_inverse(row_sum<C>(lane_sum<C>(v[u]), ln));
-        n += live[u];
 #pragma unroll
         for (int i = 0; i < C::N; ++i) acc[i] += v[u][i] * inv;
       }
