@@ -421,60 +421,154 @@ int cluster_size(int64_t T, int K) {
 }
 
 // ---------------------------------------------------------------- one row per request
+// A cluster of 8 CTAs per row.  CTA j sums x A over its eighth of K in fp32: A is read as it
+// lies, 16 bytes (eight ranks of one K row) a thread, GP = 2^k >= r / 8 threads side by side
+// on a K row, so that lanes GP apart hold the same ranks and a warp is summed by shuffles,
+// the warps and then the CTAs (through distributed shared memory) in a fixed order.  Then each
+// CTA adds its eighth of the columns: a thread takes eight columns of some rows of B.  All of
+// A's and the first rows of B's bytes are asked for before the sum is known: a row waits for
+// memory twice (adapter id, then A and B together), not three times.
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCluster = 8;
+constexpr int kAhead = 8;             // 16-byte pieces of A a thread asks for at once
+constexpr int kAheadB = 4;            // and of B
 
-__global__ void __launch_bounds__(kThreads) lora_single_kernel(const LoraArgs a) {
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__global__ void __launch_bounds__(kThreads) lora_single_kernel(const LoraArgs a, int gp, int cp) {
   pdl_begin();
-  __shared__ float s_red[kThreads * 8];
+  __shared__ float s_x[kThreads * kAhead];     // x of a pass: kThreads / gp * kAhead values at most
+  __shared__ float s_warp[kWarps][128];
+  __shared__ float s_part[kCluster][128];      // every CTA's sum over its share of K
   __shared__ float s_xa[128];
-  const int64_t row = blockIdx.x;
+  __shared__ float s_out[kThreads * 8];
+  const int64_t row = blockIdx.x / kCluster;
+  const int rank = (int)cluster_ctarank();
   const int ad = a.adapters[row];
-  if (ad < 0) return;
+  if (ad < 0) return;                          // (the same for the cluster)
   if (ad >= a.n_adapters) {
     if (threadIdx.x == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
     return;
   }
-  const int tid = threadIdx.x;
-  const int groups = a.r / 8, lanes = kThreads / groups;     // rank groups of 8, rows of A at a time
-  const int g = tid % groups, kl = tid / groups;
+  const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
   const __nv_bfloat16* A = a.A + (int64_t)ad * a.K * a.r;
   const __nv_bfloat16* B = a.B + (int64_t)ad * a.r * a.N;
   const __nv_bfloat16* X = a.X + row * a.ldx;
+
+  // ---- this CTA's columns: 8 a thread in cp threads, the rows of B over the others
+  const int ng = a.N / 8, ng_c = (ng + kCluster - 1) / kCluster;      // groups of 8 columns
+  const int g0 = rank * ng_c, g1 = g0 + ng_c < ng ? g0 + ng_c : ng;
+  const int col = tid & (cp - 1), part = tid / cp, parts = kThreads / cp;
+  const auto b_piece = [&](int g, int j) { return B + (int64_t)j * a.N + (int64_t)g * 8; };
+  // ---- this CTA's share of K
+  const int kc = ((a.K + kCluster - 1) / kCluster + 7) / 8 * 8;
+  const int k0 = rank * kc, k1 = k0 + kc < a.K ? k0 + kc : a.K;
+  const int g = tid & (gp - 1), kl = tid / gp, lanes = kThreads / gp;
+  const bool has = g * 8 < a.r;
   float acc[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) acc[c] = 0.f;
-  if (kl < lanes) {
-    for (int k = kl; k < a.K; k += lanes) {
+  uint4 bv[kAheadB];
+  const auto load_b = [&](int gb, int jb) {
+#pragma unroll
+    for (int i = 0; i < kAheadB; ++i) {
+      const int j = jb + i * parts;
+      bv[i] = gb + col < g1 && j < a.r ? ld_stream(b_piece(gb + col, j)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  // the element of Y that this thread writes first
+  const int yi = g0 + tid / 8;
+  __nv_bfloat16* y0p = a.Y + row * a.ldy + (int64_t)g0 * 8 + tid;
+  const bool y0in = tid < cp * 8 && yi < g1;
+  float y0 = 0.f;
+  if (k0 >= k1) load_b(g0, part);              // (a share of K may be empty)
+  for (int kb = k0; kb < k1; kb += lanes * kAhead) {
+    uint4 av[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = kb + i * lanes + kl;
+      av[i] = has && k < k1 ? ld_stream(A + (int64_t)k * a.r + g * 8) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (kb == k0) load_b(g0, part);
+    const int nx = k1 - kb < lanes * kAhead ? k1 - kb : lanes * kAhead;
+    if (kb != k0) __syncthreads();             // the last pass's x is read
+    for (int i = tid; i < nx; i += kThreads) s_x[i] = __bfloat162float(X[kb + i]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int o = i * lanes + kl;
+      if (o >= nx) break;
+      const float x = s_x[o];
       float v[8];
-      unpack8(*reinterpret_cast<const uint4*>(A + (int64_t)k * a.r + g * 8), v);
-      const float x = __bfloat162float(X[k]);
+      unpack8(av[i], v);
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[c] += x * v[c];
     }
   }
+  for (int o = gp; o < 32; o <<= 1) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c) s_red[tid * 8 + c] = acc[c];
-  __syncthreads();
-  if (tid < a.r) {
-    float sum = 0.f;
-    for (int l = 0; l < lanes; ++l) sum += s_red[(l * groups + tid / 8) * 8 + (tid & 7)];
-    s_xa[tid] = sum * a.scale[ad];
+    for (int c = 0; c < 8; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], o);
+  }
+  if (lane < gp && has) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) s_warp[warp][g * 8 + c] = acc[c];
   }
   __syncthreads();
-  for (int n = tid * 8; n < a.N; n += kThreads * 8) {
-    uint4* p = reinterpret_cast<uint4*>(a.Y + row * a.ldy + n);
-    float y[8], v[8];
+  if (tid < a.r) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) v += s_warp[i][tid];
+    const uint32_t mine = smem_u32(&s_part[rank][tid]);
+#pragma unroll
+    for (int q = 0; q < kCluster; ++q) st_cluster_f32(mapa_smem(mine, (uint32_t)q), v);
+  }
+  if (y0in) y0 = __bfloat162float(*y0p);
+  cluster_sync();
+  if (tid < a.r) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kCluster; ++i) v += s_part[i][tid];
+    s_xa[tid] = v * a.scale[ad];
+  }
+  __syncthreads();
+  for (int gb = g0; gb < g1; gb += cp) {
+    float y[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) y[c] = 0.f;
-    for (int j = 0; j < a.r; ++j) {
-      unpack8(*reinterpret_cast<const uint4*>(B + (int64_t)j * a.N + n), v);
+    for (int jb = part; jb < a.r; jb += parts * kAheadB) {
+      if (gb != g0 || jb != part) load_b(gb, jb);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) y[c] += s_xa[j] * v[c];
+      for (int i = 0; i < kAheadB; ++i) {
+        const int j = jb + i * parts;
+        if (j >= a.r) break;
+        const float x = s_xa[j];
+        float v[8];
+        unpack8(bv[i], v);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) y[c] += x * v[c];
+      }
     }
-    unpack8(*p, v);
+    // the parts of a column group side by side, summed in order
+    if (gb != g0) __syncthreads();
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] += y[c];
-    *p = pack8(v);
+    for (int c = 0; c < 8; ++c) s_out[(c * parts + part) * cp + col] = y[c];
+    __syncthreads();
+    for (int i = tid; i < cp * 8; i += kThreads) {
+      const int gi = gb + i / 8, c = i & 7;
+      if (gi < g1) {
+        float v = 0.f;
+        for (int q = 0; q < parts; ++q) v += s_out[(c * parts + q) * cp + i / 8];
+        __nv_bfloat16* p = a.Y + row * a.ldy + (int64_t)gi * 8 + c;
+        *p = __float2bfloat16_rn((gb == g0 && i == tid ? y0 : __bfloat162float(*p)) + v);
+      }
+    }
   }
 }
 
@@ -519,7 +613,11 @@ extern "C" moe_status_t moe_lora_requests(const moe_bf16_t* X, int64_t ldx, cons
   cudaError_t e;
   if (seq_offsets == nullptr) {
     ProfScope ps(K_LORA_REQUESTS, s);
-    e = launch_pdl(lora_single_kernel, dim3((unsigned)S), dim3(kThreads), 0, s, 1, a);
+    // threads side by side on a K row of A, and on a CTA's column groups of B
+    int gp = 1, cp = 1;
+    while (gp < r / 8) gp *= 2;
+    while (cp < kThreads && cp < (N / 8 + kCluster - 1) / kCluster) cp *= 2;
+    e = launch_pdl(lora_single_kernel, dim3((unsigned)S * kCluster), dim3(kThreads), 0, s, kCluster, a, gp, cp);
   } else {
     const int cl = cluster_size(T, K);
     e = r <= 16 ? launch_tiles<16>(a, cl, s) : r <= 32 ? launch_tiles<32>(a, cl, s)
