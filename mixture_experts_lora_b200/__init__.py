@@ -290,48 +290,53 @@ def moe_profile_read() -> dict:
 
 
 # ---------------------------------------------------------------- balance loss
-def _need(name, t, dtype, shape, device):
-    """A contiguous tensor of this type and shape on this device, or ValueError."""
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+# (These calls run beside kernels of a few microseconds, so their checks are kept to a few
+# attribute reads per tensor, and pointers go through ctypes as plain integers.)
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 
 
-def _on(t, name, stream):
-    """The stream to launch on for tensors of t's device: `stream`, or that device's current one."""
-    if not t.is_cuda:
+def _need(name, t, dtype, shape, index):
+    """A contiguous tensor of this type and shape on CUDA device `index`, or ValueError."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _index_of(name, t):
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be on a CUDA device")
-    return _stream(stream if stream is not None else torch.cuda.current_stream(t.device))
+    return index
 
 
-class _Device:
-    """Makes a device current for the launches inside (the library launches on the current one)."""
+def _launch(name, index, stream, *args):
+    """Calls the library's function `name` with device `index` current and, as its last argument,
+    `stream` or that device's current one."""
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        _check(name, getattr(lib(), name)(*args, raw))
+    else:
+        with torch.cuda.device(index):
+            _check(name, getattr(lib(), name)(*args, raw))
 
-    def __init__(self, device):
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _check_rows(logits, seq_offsets, token_mask, S):
     T, E = logits.shape
-    dev = logits.device
-    _need("logits", logits, torch.float32, (T, E), dev)
+    index = _index_of("logits", logits)
+    _need("logits", logits, _F32, (T, E), index)
     if seq_offsets is not None:
-        _need("seq_offsets", seq_offsets, torch.int32, (S + 1,), dev)
+        _need("seq_offsets", seq_offsets, _I32, (S + 1,), index)
     elif S != 1:
         raise ValueError("without seq_offsets there is one sequence")
     if token_mask is not None:
         if token_mask.dtype not in (torch.bool, torch.uint8):
             raise ValueError("token_mask must be bool or uint8")
-        _need("token_mask", token_mask, token_mask.dtype, (T,), dev)
-    return T, E, dev
+        _need("token_mask", token_mask, token_mask.dtype, (T,), index)
+    return T, E, index
 
 
 def moe_balance_workspace_bytes(T: int, E: int, S: int = 1) -> int:
@@ -343,19 +348,17 @@ def moe_balance_loss(logits, topk_ids, loss, counts, n_tokens, ws, seq_offsets=N
     """Balance loss [S] of the router for every sequence of a packed batch, with the pairs per
     expert counts [S, E] and the valid rows n_tokens [S] (see include/moelora.h)."""
     S = loss.shape[0]
-    T, E, dev = _check_rows(logits, seq_offsets, token_mask, S)
+    T, E, index = _check_rows(logits, seq_offsets, token_mask, S)
     k = topk_ids.shape[1]
-    _need("topk_ids", topk_ids, torch.int32, (T, k), dev)
-    _need("loss", loss, torch.float32, (S,), dev)
-    _need("counts", counts, torch.int32, (S, E), dev)
-    _need("n_tokens", n_tokens, torch.int32, (S,), dev)
-    if ws.device != dev:
-        raise ValueError(f"the workspace must be on {dev}")
-    st = _on(logits, "logits", stream)
-    with _Device(dev):
-        _check("moe_balance_loss", lib().moe_balance_loss(
-            _ptr(logits), _ptr(topk_ids), T, E, k, _ptr(seq_offsets), S, _ptr(token_mask), _ptr(loss),
-            _ptr(counts), _ptr(n_tokens), _ptr(ws), ws.numel() * ws.element_size(), st))
+    _need("topk_ids", topk_ids, _I32, (T, k), index)
+    _need("loss", loss, _F32, (S,), index)
+    _need("counts", counts, _I32, (S, E), index)
+    _need("n_tokens", n_tokens, _I32, (S,), index)
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on cuda:{index}")
+    _launch("moe_balance_loss", index, stream, logits.data_ptr(), topk_ids.data_ptr(), T, E, k,
+            _addr(seq_offsets), S, _addr(token_mask), loss.data_ptr(), counts.data_ptr(), n_tokens.data_ptr(),
+            ws.data_ptr(), ws.nbytes)
 
 
 def moe_balance_loss_backward(logits, counts, n_tokens, dloss, k, dlogits, seq_offsets=None,
@@ -363,16 +366,14 @@ def moe_balance_loss_backward(logits, counts, n_tokens, dloss, k, dlogits, seq_o
     """Gradient of moe_balance_loss into the logits for the upstream gradient dloss [S], written
     to dlogits [T, E] or added to it."""
     S = dloss.shape[0]
-    T, E, dev = _check_rows(logits, seq_offsets, token_mask, S)
-    _need("counts", counts, torch.int32, (S, E), dev)
-    _need("n_tokens", n_tokens, torch.int32, (S,), dev)
-    _need("dloss", dloss, torch.float32, (S,), dev)
-    _need("dlogits", dlogits, torch.float32, (T, E), dev)
-    st = _on(logits, "logits", stream)
-    with _Device(dev):
-        _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
-            _ptr(logits), _ptr(counts), _ptr(n_tokens), _ptr(dloss), T, E, int(k), _ptr(seq_offsets), S,
-            _ptr(token_mask), _ptr(dlogits), 1 if accumulate else 0, st))
+    T, E, index = _check_rows(logits, seq_offsets, token_mask, S)
+    _need("counts", counts, _I32, (S, E), index)
+    _need("n_tokens", n_tokens, _I32, (S,), index)
+    _need("dloss", dloss, _F32, (S,), index)
+    _need("dlogits", dlogits, _F32, (T, E), index)
+    _launch("moe_balance_loss_backward", index, stream, logits.data_ptr(), counts.data_ptr(), n_tokens.data_ptr(),
+            dloss.data_ptr(), T, E, int(k), _addr(seq_offsets), S, _addr(token_mask), dlogits.data_ptr(),
+            1 if accumulate else 0)
 
 
 # ---------------------------------------------------------------- adapters of many requests
@@ -383,26 +384,25 @@ def moe_lora_requests(X, adapters, A, B, scale, Y, seq_offsets=None, stream=None
     T, K = X.shape
     n, _, r = A.shape
     N = Y.shape[1]
-    dev = X.device
     S = adapters.shape[0]
-    for name, t, w in (("X", X, K), ("Y", Y, N)):
-        if (t.dtype != torch.bfloat16 or t.shape[0] != T or t.device != dev or (w > 1 and t.stride(1) != 1)):
-            raise ValueError(f"{name} must be bfloat16 [{T}, {w}] on {dev} with unit stride inside its rows")
-    _need("A", A, torch.bfloat16, (n, K, r), dev)
-    _need("B", B, torch.bfloat16, (n, r, N), dev)
-    _need("scale", scale, torch.float32, (n,), dev)
-    _need("adapters", adapters, torch.int32, (S,), dev)
+    index = _index_of("X", X)
+    sx, sy = X.stride(), Y.stride()
+    if X.dtype is not _BF16 or sx[1] != 1:
+        raise ValueError("X must be bfloat16 with unit stride inside its rows")
+    if Y.dtype is not _BF16 or Y.shape[0] != T or sy[1] != 1 or Y.get_device() != index:
+        raise ValueError(f"Y must be bfloat16 of {T} rows on cuda:{index} with unit stride inside its rows")
+    _need("A", A, _BF16, (n, K, r), index)
+    _need("B", B, _BF16, (n, r, N), index)
+    _need("scale", scale, _F32, (n,), index)
+    _need("adapters", adapters, _I32, (S,), index)
     if seq_offsets is not None:
-        _need("seq_offsets", seq_offsets, torch.int32, (S + 1,), dev)
+        _need("seq_offsets", seq_offsets, _I32, (S + 1,), index)
     elif S != T:
         raise ValueError("without seq_offsets every row is a request: adapters must have one entry per row")
-    st = _on(X, "X", stream)
     # (the stride of a single row means nothing)
-    ldx, ldy = (X.stride(0), Y.stride(0)) if T > 1 else (K, N)
-    with _Device(dev):
-        _check("moe_lora_requests", lib().moe_lora_requests(
-            _ptr(X), ldx, _ptr(seq_offsets), _ptr(adapters), T, S, _ptr(A), _ptr(B), _ptr(scale), n, K, N, r,
-            _ptr(Y), ldy, st))
+    ldx, ldy = (sx[0], sy[0]) if T > 1 else (K, N)
+    _launch("moe_lora_requests", index, stream, X.data_ptr(), ldx, _addr(seq_offsets), adapters.data_ptr(), T, S,
+            A.data_ptr(), B.data_ptr(), scale.data_ptr(), n, K, N, r, Y.data_ptr(), ldy)
 
 
 # ---------------------------------------------------------------- AdamW
@@ -450,8 +450,7 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
         self.device = dev = self.params[0].device
-        if dev.type != "cuda":
-            raise ValueError("parameters must be on a CUDA device")
+        self.index = _index_of("parameters", self.params[0])
         self.lr, self.state_bits = lr, state_bits
         ok = (torch.bfloat16, torch.float32)
         groups, taken, at = {}, set(), 0
@@ -487,6 +486,7 @@ class AdamW:
             for i in (i for g, idx in groups.items() if g[2] for i in idx):
                 self._part(self.master, i).copy_(self.params[i])
         self._count = torch.zeros(2, dtype=torch.int64, device=dev)
+        self._count_ptr = self._count.data_ptr()
         self.steps = self._count[0]
         elem = 1 if state_bits == 8 else 4
         self._calls = []
@@ -505,7 +505,7 @@ class AdamW:
                     row.size[d], row.param_stride[d], row.grad_stride[d] = n, sp, sg
             cfg = moe_adamw_config_t(0.0, betas[0], betas[1], eps, weight_decay, int(p16), int(g16), int(master),
                                      state_bits)
-            self._calls.append((table, len(idx), cfg, ctypes.byref(cfg)))
+            self._calls.append((table, len(idx), cfg, ctypes.byref(cfg), int(len(self._calls) == len(groups) - 1)))
 
     def _part(self, flat, i):
         p = self.params[i]
@@ -514,21 +514,21 @@ class AdamW:
     def step(self, grad_scale=None, stream=None):
         """One step with the gradients in the buffers, times grad_scale (a device fp32 tensor of
         one element) where given."""
+        lr, scale = self.lr, None
         lr_dev = None
-        if isinstance(self.lr, torch.Tensor):
-            lr_dev = self.lr
-            _need("lr", lr_dev, torch.float32, tuple(lr_dev.shape) if lr_dev.numel() == 1 else (1,), self.device)
+        if isinstance(lr, torch.Tensor):
+            self._scalar("lr", lr)
+            lr, lr_dev = 0.0, lr.data_ptr()
         if grad_scale is not None:
-            _need("grad_scale", grad_scale, torch.float32,
-                  tuple(grad_scale.shape) if grad_scale.numel() == 1 else (1,), self.device)
-        st = _on(self._count, "parameters", stream)
-        last = len(self._calls) - 1
-        fn, count = lib().moe_adamw_step, _ptr(self._count)
-        with _Device(self.device):
-            for j, (table, n, cfg, ref) in enumerate(self._calls):
-                if lr_dev is None:
-                    cfg.lr = self.lr
-                _check("moe_adamw_step", fn(table, n, ref, _ptr(lr_dev), _ptr(grad_scale), count, int(j == last), st))
+            self._scalar("grad_scale", grad_scale)
+            scale = grad_scale.data_ptr()
+        for table, n, cfg, ref, last in self._calls:
+            cfg.lr = lr
+            _launch("moe_adamw_step", self.index, stream, table, n, ref, lr_dev, scale, self._count_ptr, last)
+
+    def _scalar(self, name, t):
+        if t.dtype is not _F32 or t.numel() != 1 or t.get_device() != self.index:
+            raise ValueError(f"{name} must be a float32 tensor of one element on cuda:{self.index}")
 
     def moments(self, i: int):
         """(m, v) of parameter i as fp32 tensors of its shape (what the codes stand for in 8 bits)."""
