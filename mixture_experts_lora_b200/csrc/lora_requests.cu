@@ -30,6 +30,9 @@
 namespace moe {
 namespace {
 
+// Requests of up to this many rows are worked through row by row.
+constexpr int kShortRows = 4;
+
 struct LoraArgs {
   const __nv_bfloat16* X;
   int64_t ldx;
@@ -44,31 +47,6 @@ struct LoraArgs {
   __nv_bfloat16* Y;
   int64_t ldy;
   int* err;
-};
-
-// ---------------------------------------------------------------- rows of one adapter
-template <int RP_>
-struct TilesCfg {
-  static constexpr int RP = RP_;
-  static constexpr int BM = 128, BK = 64, BN = 64;
-  static constexpr int ROWS_BYTES = BM * 64 * 2;          // X or Y rows of a stage
-  static constexpr int AD_BYTES = RP * 64 * 2;            // A or B of a stage
-  static constexpr int STAGE_BYTES = ROWS_BYTES + AD_BYTES;
-  static constexpr int STAGES = RP == 128 ? 3 : 4;
-  static constexpr int OP_ATOMS = RP <= 32 ? 1 : 2 * RP / 64;   // 64-column atoms of [hi | lo]
-  static constexpr int OP_BYTES = OP_ATOMS * BM * 128;
-  static constexpr int PART_BYTES = BM * RP * 4;          // exchanged partial (clusters only)
-  static constexpr int BAR_BYTES = 256;
-  static constexpr int TMEM_COLS = 128;                   // two 64-column accumulators; S before them
-  static constexpr int THREADS = 192;                     // epilogue warps 0-3, loader, MMA issuer
-  static int smem_bytes(bool cluster) {
-    return STAGES * STAGE_BYTES + OP_BYTES + (cluster ? PART_BYTES : 0) + BAR_BYTES + 1024;
-  }
-  // A chunk [64 K rows][RP], rank innermost: rows of up to 128 bytes, two atoms at rank 128
-  static constexpr uint32_t A_SW = RP == 16 ? kSw32 : RP == 32 ? kSw64 : kSw128;
-  static constexpr int A_ROWB = (RP < 64 ? RP : 64) * 2;
-  static constexpr int A_ATOMS = RP > 64 ? 2 : 1;
-  static constexpr int A_ATOM_BYTES = BK * A_ROWB;
 };
 
 __device__ __forceinline__ uint32_t cluster_nctarank() {
@@ -94,8 +72,261 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// mbarriers that CTAs of a cluster arrive on for one another: the waiter sees what the
+// arriving threads wrote.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, int* err) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 31u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
+      report_error(err, MOE_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- one row
+// One row x by a cluster.  CTA j sums x A over its share of K in fp32: A is read as it lies,
+// 16 bytes (eight ranks of one K row) a thread, GP = 2^k >= r / 8 threads side by side on a K
+// row, so that lanes GP apart hold the same ranks and a warp is summed by shuffles, the warps
+// and then the CTAs (through distributed shared memory) in a fixed order.  Then each CTA adds
+// its share of the columns: a thread takes eight columns of some rows of B.
+// A row is a chain of waits for memory, each of 1 us and under load of 3: everything whose
+// address is known goes out together (A, x, the scale and the first two rounds of B once the
+// adapter's id is there, Y before the CTAs meet), and A and B run two buffers ahead.
+constexpr int kAhead = 4;             // 16-byte pieces of A (and of B) in one of two buffers
+constexpr int kXChunk = 2048;         // values of x staged at a time
+constexpr int kMaxCluster = 8;
+
+template <int NT>
+struct RowSmem {
+  float x[kXChunk];
+  float warp[NT / 32][128];
+  float part[2][kMaxCluster][128];    // every CTA's sum over its share of K, rows in turn
+  float xa[128];
+  float4 out[2][NT];                  // partial sums of eight columns
+};
+
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void add_scaled(float (&y)[8], uint4 w, float x) {
+  float v[8];
+  unpack8(w, v);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) y[c] += x * v[c];
+}
+
+template <int NT>
+__device__ __forceinline__ void single_row(const LoraArgs& a, int64_t row, int ad, int rank, int CL, int turn,
+                                           RowSmem<NT>& sm) {
+  const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
+  const float scale = a.scale[ad];
+  // ---- this CTA's share of K: thread (kl, g) reads ranks 8 g .. of K rows kl, kl + lanes, ...
+  int gp = 1;
+  while (gp < a.r / 8) gp *= 2;
+  const int kc = ((a.K + CL - 1) / CL + 7) / 8 * 8;
+  const int k0 = rank * kc < a.K ? rank * kc : a.K, k1 = k0 + kc < a.K ? k0 + kc : a.K;
+  const int g = tid & (gp - 1), kl = tid / gp, lanes = NT / gp;
+  const bool has = g * 8 < a.r;
+  const __nv_bfloat16* A = a.A + ((int64_t)ad * a.K + k0 + kl) * a.r + g * 8;
+  const int64_t a_step = (int64_t)lanes * a.r;
+  const int np = (k1 - k0 + lanes - 1) / lanes;                       // pieces (of any thread)
+  const int px = (kXChunk / lanes) & ~(kAhead - 1);                   // pieces per chunk of x
+  uint4 av[2][kAhead];
+  const auto load_a = [&](int p, uint4 (&v)[kAhead]) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      v[i] = has && k0 + kl + (p + i) * lanes < k1 ? ld_stream(A + (p + i) * a_step) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  // ---- this CTA's columns: eight a thread, cp threads side by side, the rows of B over the
+  // others; passes of cp column groups, each in rounds of kAhead rows
+  const int ng = a.N / 8, ng_c = (ng + CL - 1) / CL;
+  const int g0 = rank * ng_c, g1 = g0 + ng_c < ng ? g0 + ng_c : ng;
+  int cp = 32;
+  while (cp * 2 <= (NT & -NT) && cp < ng_c) cp *= 2;
+  const int col = tid & (cp - 1), part = tid / cp, parts = NT / cp;
+  const int rounds = (a.r + parts * kAhead - 1) / (parts * kAhead);
+  const int passes = g1 > g0 ? (g1 - g0 + cp - 1) / cp : 0;
+  const __nv_bfloat16* B = a.B + (int64_t)ad * a.r * a.N;
+  uint4 bv[2][kAhead];
+  const auto load_b = [&](int pass, int round, uint4 (&v)[kAhead]) {
+    const int gi = g0 + pass * cp + col;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = (round * kAhead + i) * parts + part;
+      v[i] = pass < passes && gi < g1 && j < a.r ? ld_stream(B + (int64_t)j * a.N + (int64_t)gi * 8)
+                                                : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  load_a(0, av[0]);
+  load_a(kAhead, av[1]);
+  load_b(0, 0, bv[0]);
+  load_b(rounds > 1 ? 0 : 1, rounds > 1 ? 1 : 0, bv[1]);
+
+  float acc[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+  const __nv_bfloat16* X = a.X + row * a.ldx + k0;
+  for (int p0 = 0; p0 < np; p0 += px) {
+    // x of px pieces (k0, the chunk and K are multiples of 8)
+    const int nx = k1 - k0 - p0 * lanes < px * lanes ? k1 - k0 - p0 * lanes : px * lanes;
+    __syncthreads();
+    for (int i = tid * 8; i < nx; i += NT * 8) {
+      float v[8];
+      unpack8(*reinterpret_cast<const uint4*>(X + p0 * lanes + i), v);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sm.x[i + c] = v[c];
+    }
+    __syncthreads();
+    const int pe = np - p0 < px ? np - p0 : px;
+    for (int p = 0; p < pe; p += 2 * kAhead) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int o = (p + h * kAhead + i) * lanes + kl;
+          add_scaled(acc, av[h][i], o < nx ? sm.x[o] : 0.f);
+        }
+        load_a(p0 + p + (2 + h) * kAhead, av[h]);
+      }
+    }
+  }
+  for (int o = gp; o < 32; o <<= 1) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], o);
+  }
+  if (lane < gp && has) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) sm.warp[warp][g * 8 + c] = acc[c];
+  }
+  __syncthreads();
+  if (tid < a.r) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) v += sm.warp[i][tid];
+    const uint32_t mine = smem_u32(&sm.part[turn & 1][rank][tid]);
+    for (int q = 0; q < CL; ++q) st_cluster_f32(mapa_smem(mine, (uint32_t)q), v);
+  }
+  // the eight elements of Y that this thread finishes in a pass
+  uint4* yp = reinterpret_cast<uint4*>(a.Y + row * a.ldy) + g0 + tid;
+  const auto ends = [&](int pass) { return tid < cp && g0 + pass * cp + tid < g1; };
+  uint4 yv = make_uint4(0u, 0u, 0u, 0u);
+  if (ends(0)) yv = *yp;
+  cluster_sync();
+  if (tid < a.r) {
+    float v = 0.f;
+    for (int i = 0; i < CL; ++i) v += sm.part[turn & 1][i][tid];
+    sm.xa[tid] = v * scale;
+  }
+  __syncthreads();
+  int next_pass = 0, next_round = 0;      // two rounds ahead
+  const auto advance = [&]() {
+    if (++next_round == rounds) { next_round = 0; ++next_pass; }
+  };
+  advance();
+  advance();
+  int h = 0;
+  for (int pass = 0; pass < passes; ++pass) {
+    float y[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) y[c] = 0.f;
+    for (int round = 0; round < rounds; ++round, h ^= 1) {
+      uint4 v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) v[i] = h ? bv[1][i] : bv[0][i];
+      if (h) load_b(next_pass, next_round, bv[1]);
+      else load_b(next_pass, next_round, bv[0]);
+      advance();
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = (round * kAhead + i) * parts + part;
+        add_scaled(y, v[i], j < a.r ? sm.xa[j] : 0.f);
+      }
+    }
+    // the parts of a column group, summed in order
+    if (pass > 0) __syncthreads();
+    sm.out[0][tid] = make_float4(y[0], y[1], y[2], y[3]);
+    sm.out[1][tid] = make_float4(y[4], y[5], y[6], y[7]);
+    __syncthreads();
+    if (ends(pass)) {
+      float v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = 0.f;
+      for (int q = 0; q < parts; ++q) {
+        const float4 lo = sm.out[0][q * cp + tid], hi = sm.out[1][q * cp + tid];
+        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+      }
+      float old[8];
+      unpack8(yv, old);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] += old[c];
+      yp[pass * cp] = pack8(v);
+      if (ends(pass + 1)) yv = yp[(pass + 1) * cp];
+    }
+  }
+}
+
+// One row per request (seq_offsets = NULL): a cluster per row.
+constexpr int kSingleThreads = 256;
+__global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraArgs a) {
+  pdl_begin();
+  __shared__ RowSmem<kSingleThreads> sm;
+  const int rank = (int)cluster_ctarank(), CL = (int)cluster_nctarank();
+  const int64_t row = (int)blockIdx.x / CL;
+  const int ad = a.adapters[row];
+  if (ad < 0) return;                          // (the same for the cluster)
+  if (ad >= a.n_adapters) {
+    if (threadIdx.x == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
+    return;
+  }
+  single_row<kSingleThreads>(a, row, ad, rank, CL, 0, sm);
+}
+
+// ---------------------------------------------------------------- rows of one adapter
+template <int RP_>
+struct TilesCfg {
+  static constexpr int RP = RP_;
+  static constexpr int BM = 128, BK = 64, BN = 64;
+  static constexpr int ROWS_BYTES = BM * 64 * 2;          // X or Y rows of a stage
+  static constexpr int AD_BYTES = RP * 64 * 2;            // A or B of a stage
+  static constexpr int STAGE_BYTES = ROWS_BYTES + AD_BYTES;
+  // with a cluster's PART buffer two CTAs per SM up to rank 32
+  static constexpr int STAGES = RP == 32 || RP == 128 ? 3 : 4;
+  static constexpr int OP_ATOMS = RP <= 32 ? 1 : 2 * RP / 64;   // 64-column atoms of [hi | lo]
+  static constexpr int OP_BYTES = OP_ATOMS * BM * 128;
+  static constexpr int PART_BYTES = BM * RP * 4;          // exchanged partial (clusters only)
+  static constexpr int BAR_BYTES = 256;
+  static constexpr int TMEM_COLS = 128;                   // two 64-column accumulators; S before them
+  static constexpr int THREADS = 192;                     // epilogue warps 0-3, loader, MMA issuer
+  static int smem_bytes(bool cluster) {
+    return STAGES * STAGE_BYTES + OP_BYTES + (cluster ? PART_BYTES : 0) + BAR_BYTES + 1024;
+  }
+  static_assert(sizeof(RowSmem<THREADS>) <= STAGES * STAGE_BYTES, "short requests use the ring's memory");
+  // A chunk [64 K rows][RP], rank innermost: rows of up to 128 bytes, two atoms at rank 128
+  static constexpr uint32_t A_SW = RP == 16 ? kSw32 : RP == 32 ? kSw64 : kSw128;
+  static constexpr int A_ROWB = (RP < 64 ? RP : 64) * 2;
+  static constexpr int A_ATOMS = RP > 64 ? 2 : 1;
+  static constexpr int A_ATOM_BYTES = BK * A_ROWB;
+};
+
+// (Registers are given to warps in fours, so two blocks of six warps hold as many as two of
+// eight: at most 128 a thread.)
 template <class C>
-__global__ void __launch_bounds__(C::THREADS)
+__global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
     lora_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmY,
                       const LoraArgs a) {
@@ -113,7 +344,9 @@ __global__ void __launch_bounds__(C::THREADS)
   uint64_t* acc_done = bars + 3 * S + 4;
   uint64_t* op_ready = bars + 3 * S + 5;
   uint64_t* drain = bars + 3 * S + 6;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 7);
+  uint64_t* peer_ready = bars + 3 * S + 7;   // every CTA's partial is written (4 warps each)
+  uint64_t* part_read = bars + 3 * S + 8;    // this CTA's partial is read by every CTA
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 9);
 
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
   const int rank = (int)cluster_ctarank(), CL = (int)cluster_nctarank();
@@ -130,6 +363,8 @@ __global__ void __launch_bounds__(C::THREADS)
     mbar_init(smem_u32(acc_done), 1);
     mbar_init(smem_u32(op_ready), C::BM);
     mbar_init(smem_u32(drain), 1);
+    mbar_init(smem_u32(peer_ready), 4 * CL);
+    mbar_init(smem_u32(part_read), 4 * CL);
     mbar_fence_init();
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmA);
@@ -137,15 +372,31 @@ __global__ void __launch_bounds__(C::THREADS)
     tma_prefetch_desc(&tmY);
   }
   pdl_begin();
-  // the cluster's tile, the same for all its CTAs: slot -> (window, request) -> rows, adapter
-  const int slot = (int)blockIdx.x / CL;
   check_offsets(a.off, a.S, a.T, a.err);
+  // the last S clusters take the short requests, row by row
+  const int slot = (int)blockIdx.x / CL, tiles = (int)gridDim.x / CL - a.S;
+  if (slot >= tiles) {
+    const int64_t lo = a.off[slot - tiles], hi = a.off[slot - tiles + 1];
+    const int ad = a.adapters[slot - tiles];
+    if (hi <= lo || hi - lo > kShortRows || lo < 0 || hi > a.T || ad < 0) return;
+    if (ad >= a.n_adapters) {
+      if (tid == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
+      return;
+    }
+    RowSmem<C::THREADS>& sm = *reinterpret_cast<RowSmem<C::THREADS>*>(smem);
+    for (int64_t t = lo; t < hi; ++t) {
+      if (t > lo) __syncthreads();
+      single_row<C::THREADS>(a, t, ad, rank, CL, (int)(t - lo), sm);
+    }
+    return;
+  }
+  // the others a tile, the same for all CTAs: slot -> (window, request) -> rows, adapter
   const int s = block_count_le(a.S, slot, [&](int i) { return (long long)a.off[i] / C::BM + i; }) - 1;
   if (s < 0) return;
   const int64_t w = slot - s, lo = a.off[s], hi = a.off[s + 1];
   const int64_t row0 = w * C::BM;
   const int64_t r0 = row0 > lo ? row0 : lo, r1 = row0 + C::BM < hi ? row0 + C::BM : hi;
-  if (lo < 0 || r1 > a.T || r0 >= r1) return;
+  if (lo < 0 || r1 > a.T || r0 >= r1 || hi - lo <= kShortRows) return;
   const int ad = a.adapters[s];
   if (ad < 0) return;
   if (ad >= a.n_adapters) {
@@ -167,10 +418,10 @@ __global__ void __launch_bounds__(C::THREADS)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
+  if (CL > 1) cluster_arrive();        // this CTA's barriers are there for the others' arrivals
 
   if (warp == 4) {
     // ------------------------------------------------------------ loader
-    if (CL > 1) cluster_arrive();
     if (lane == 0) {
       const uint32_t bytes = (uint32_t)(box1 - box0) * 32 * 128 + C::AD_BYTES;
       int it = 0;
@@ -207,7 +458,6 @@ __global__ void __launch_bounds__(C::THREADS)
     __syncwarp();
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
-    if (CL > 1) cluster_arrive();
     if (lane == 0) {
       const uint32_t id1 = idesc_bf16(128, RP, 0, 1), id2 = idesc_bf16(128, C::BN, 0, 1);
       for (int it = 0; it < n_x && ok; ++it) {
@@ -271,8 +521,10 @@ __global__ void __launch_bounds__(C::THREADS)
               make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
       }
       __syncwarp();
-      cluster_arrive();
-      cluster_wait();
+      cluster_wait();                  // (long past: every CTA has set up its barriers)
+      if (lane < CL) mbar_arrive_cluster(mapa_smem(smem_u32(peer_ready), (uint32_t)lane));
+      if (!mbar_wait_cluster(smem_u32(peer_ready), 0, a.err)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
     }
 #pragma unroll 1
     for (int c0 = 0; c0 < RP; c0 += 16) {
@@ -280,12 +532,22 @@ __global__ void __launch_bounds__(C::THREADS)
       if (CL > 1) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = 0.f;
-        for (int q = 0; q < CL; ++q) {
+        float4 v[4][4];                // (the loads of all CTAs' partials together)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (q >= CL) break;
           const uint32_t base = mapa_smem(smem_u32(part + tid * RP), (uint32_t)q);
 #pragma unroll
+          for (int g = 0; g < 4; ++g)
+            v[q][g] = ld_cluster_f4(base + (((c0 / 4 + g) ^ (tid & (PIECES - 1))) * 16));
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (q >= CL) break;
+#pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const float4 v = ld_cluster_f4(base + (((c0 / 4 + g) ^ (tid & (PIECES - 1))) * 16));
-            x[4 * g] += v.x; x[4 * g + 1] += v.y; x[4 * g + 2] += v.z; x[4 * g + 3] += v.w;
+            x[4 * g] += v[q][g].x; x[4 * g + 1] += v[q][g].y;
+            x[4 * g + 2] += v[q][g].z; x[4 * g + 3] += v[q][g].w;
           }
         }
       } else {
@@ -311,6 +573,10 @@ __global__ void __launch_bounds__(C::THREADS)
               pack8(p == 0 ? h : l);
         }
       }
+    }
+    if (CL > 1) {
+      __syncwarp();
+      if (lane < CL) mbar_arrive_cluster(mapa_smem(smem_u32(part_read), (uint32_t)lane));
     }
     tc_fence_before();
     fence_proxy_async_smem();
@@ -374,11 +640,10 @@ __global__ void __launch_bounds__(C::THREADS)
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
   }
-  // everybody is done with its own pipes, and with the others' partials
+  // the CTA may go once the others have read its partial
   if (CL > 1) {
     if (warp >= 4) cluster_wait();
-    cluster_arrive();
-    cluster_wait();
+    mbar_wait_cluster(smem_u32(part_read), 0, a.err);
   }
   tc_fence_before();
   __syncthreads();
@@ -406,170 +671,30 @@ cudaError_t launch_tiles(const LoraArgs& a, int CL, cudaStream_t s) {
   auto kern = lora_tiles_kernel<C>;
   cudaError_t st = ensure_smem(kern, C::smem_bytes(true));
   if (st != cudaSuccess) return st;
-  const int64_t slots = (a.T + C::BM - 1) / C::BM + a.S - 1;
+  const int64_t slots = (a.T + C::BM - 1) / C::BM + a.S - 1 + a.S;
   ProfScope ps(K_LORA_REQUESTS, s);
   return launch_pdl(kern, dim3((unsigned)(slots * CL)), dim3(C::THREADS), smem, s, CL, tx, ta, tb, ty, a);
 }
 
-// CTAs per cluster: as many as keep the windows' clusters within two CTAs per SM (the
-// occupancy at rank 16), and no more than there are 64-column stages of K to share.
+// CTAs per cluster: as many as keep the windows' clusters within two CTAs per SM (the occupancy
+// up to rank 32), no more than there are 64-column stages of K to share, and at most 4: clusters
+// of 8 find few places (15 at a time on 148 SMs; 4133 rows at 2880 x 2880, rank 16: 78 us with 8,
+// 32 us with 4, 43 us with 2).
 int cluster_size(int64_t T, int K) {
   const int64_t tiles = (T + 127) / 128;
   int cl = 1;
-  while (cl < 8 && tiles * cl * 2 <= 2 * (int64_t)device_sms() && cl * 2 <= (K + 63) / 64) cl *= 2;
+  while (cl < 4 && tiles * cl * 2 <= 2 * (int64_t)device_sms() && cl * 2 <= (K + 63) / 64) cl *= 2;
   return cl;
 }
 
-// ---------------------------------------------------------------- one row per request
-// A cluster of 8 CTAs per row.  CTA j sums x A over its eighth of K in fp32: A is read as it
-// lies, 16 bytes (eight ranks of one K row) a thread, GP = 2^k >= r / 8 threads side by side
-// on a K row, so that lanes GP apart hold the same ranks and a warp is summed by shuffles,
-// the warps and then the CTAs (through distributed shared memory) in a fixed order.  Then each
-// CTA adds its eighth of the columns: a thread takes eight columns of some rows of B.  All of
-// A's and the first rows of B's bytes are asked for before the sum is known: a row waits for
-// memory twice (adapter id, then A and B together), not three times.
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = 8;
-constexpr int kAhead = 8;             // 16-byte pieces of A a thread asks for at once
-constexpr int kAheadB = 4;            // and of B
-
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-__global__ void __launch_bounds__(kThreads) lora_single_kernel(const LoraArgs a, int gp, int cp) {
-  pdl_begin();
-  __shared__ float s_x[kThreads * kAhead];     // x of a pass: kThreads / gp * kAhead values at most
-  __shared__ float s_warp[kWarps][128];
-  __shared__ float s_part[kCluster][128];      // every CTA's sum over its share of K
-  __shared__ float s_xa[128];
-  __shared__ float s_out[kThreads * 8];
-  const int64_t row = blockIdx.x / kCluster;
-  const int rank = (int)cluster_ctarank();
-  const int ad = a.adapters[row];
-  if (ad < 0) return;                          // (the same for the cluster)
-  if (ad >= a.n_adapters) {
-    if (threadIdx.x == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
-    return;
-  }
-  const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
-  const __nv_bfloat16* A = a.A + (int64_t)ad * a.K * a.r;
-  const __nv_bfloat16* B = a.B + (int64_t)ad * a.r * a.N;
-  const __nv_bfloat16* X = a.X + row * a.ldx;
-
-  // ---- this CTA's columns: 8 a thread in cp threads, the rows of B over the others
-  const int ng = a.N / 8, ng_c = (ng + kCluster - 1) / kCluster;      // groups of 8 columns
-  const int g0 = rank * ng_c, g1 = g0 + ng_c < ng ? g0 + ng_c : ng;
-  const int col = tid & (cp - 1), part = tid / cp, parts = kThreads / cp;
-  const auto b_piece = [&](int g, int j) { return B + (int64_t)j * a.N + (int64_t)g * 8; };
-  // ---- this CTA's share of K
-  const int kc = ((a.K + kCluster - 1) / kCluster + 7) / 8 * 8;
-  const int k0 = rank * kc, k1 = k0 + kc < a.K ? k0 + kc : a.K;
-  const int g = tid & (gp - 1), kl = tid / gp, lanes = kThreads / gp;
-  const bool has = g * 8 < a.r;
-  float acc[8];
-#pragma unroll
-  for (int c = 0; c < 8; ++c) acc[c] = 0.f;
-  uint4 bv[kAheadB];
-  const auto load_b = [&](int gb, int jb) {
-#pragma unroll
-    for (int i = 0; i < kAheadB; ++i) {
-      const int j = jb + i * parts;
-      bv[i] = gb + col < g1 && j < a.r ? ld_stream(b_piece(gb + col, j)) : make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
-  // the element of Y that this thread writes first
-  const int yi = g0 + tid / 8;
-  __nv_bfloat16* y0p = a.Y + row * a.ldy + (int64_t)g0 * 8 + tid;
-  const bool y0in = tid < cp * 8 && yi < g1;
-  float y0 = 0.f;
-  if (k0 >= k1) load_b(g0, part);              // (a share of K may be empty)
-  for (int kb = k0; kb < k1; kb += lanes * kAhead) {
-    uint4 av[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int k = kb + i * lanes + kl;
-      av[i] = has && k < k1 ? ld_stream(A + (int64_t)k * a.r + g * 8) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (kb == k0) load_b(g0, part);
-    const int nx = k1 - kb < lanes * kAhead ? k1 - kb : lanes * kAhead;
-    if (kb != k0) __syncthreads();             // the last pass's x is read
-    for (int i = tid; i < nx; i += kThreads) s_x[i] = __bfloat162float(X[kb + i]);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int o = i * lanes + kl;
-      if (o >= nx) break;
-      const float x = s_x[o];
-      float v[8];
-      unpack8(av[i], v);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] += x * v[c];
-    }
-  }
-  for (int o = gp; o < 32; o <<= 1) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], o);
-  }
-  if (lane < gp && has) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) s_warp[warp][g * 8 + c] = acc[c];
-  }
-  __syncthreads();
-  if (tid < a.r) {
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) v += s_warp[i][tid];
-    const uint32_t mine = smem_u32(&s_part[rank][tid]);
-#pragma unroll
-    for (int q = 0; q < kCluster; ++q) st_cluster_f32(mapa_smem(mine, (uint32_t)q), v);
-  }
-  if (y0in) y0 = __bfloat162float(*y0p);
-  cluster_sync();
-  if (tid < a.r) {
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < kCluster; ++i) v += s_part[i][tid];
-    s_xa[tid] = v * a.scale[ad];
-  }
-  __syncthreads();
-  for (int gb = g0; gb < g1; gb += cp) {
-    float y[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) y[c] = 0.f;
-    for (int jb = part; jb < a.r; jb += parts * kAheadB) {
-      if (gb != g0 || jb != part) load_b(gb, jb);
-#pragma unroll
-      for (int i = 0; i < kAheadB; ++i) {
-        const int j = jb + i * parts;
-        if (j >= a.r) break;
-        const float x = s_xa[j];
-        float v[8];
-        unpack8(bv[i], v);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) y[c] += x * v[c];
-      }
-    }
-    // the parts of a column group side by side, summed in order
-    if (gb != g0) __syncthreads();
-#pragma unroll
-    for (int c = 0; c < 8; ++c) s_out[(c * parts + part) * cp + col] = y[c];
-    __syncthreads();
-    for (int i = tid; i < cp * 8; i += kThreads) {
-      const int gi = gb + i / 8, c = i & 7;
-      if (gi < g1) {
-        float v = 0.f;
-        for (int q = 0; q < parts; ++q) v += s_out[(c * parts + q) * cp + i / 8];
-        __nv_bfloat16* p = a.Y + row * a.ldy + (int64_t)gi * 8 + c;
-        *p = __float2bfloat16_rn((gb == g0 && i == tid ? y0 : __bfloat162float(*p)) + v);
-      }
-    }
-  }
+// CTAs per row of lora_single_kernel: 8 while all clusters find a place at once (15 of 8 CTAs),
+// then what keeps the CTAs within two per SM (64 rows at 7168 x 2048, rank 32: 14 us with 8,
+// 10.2 us with 4, 11.2 us with 2, 19 us with 1).
+int single_cluster(int64_t S) {
+  if (S <= 15) return 8;
+  int cl = 4;
+  while (cl > 1 && S * cl > 2 * (int64_t)device_sms()) cl /= 2;
+  return cl;
 }
 
 }  // namespace
@@ -613,11 +738,8 @@ extern "C" moe_status_t moe_lora_requests(const moe_bf16_t* X, int64_t ldx, cons
   cudaError_t e;
   if (seq_offsets == nullptr) {
     ProfScope ps(K_LORA_REQUESTS, s);
-    // threads side by side on a K row of A, and on a CTA's column groups of B
-    int gp = 1, cp = 1;
-    while (gp < r / 8) gp *= 2;
-    while (cp < kThreads && cp < (N / 8 + kCluster - 1) / kCluster) cp *= 2;
-    e = launch_pdl(lora_single_kernel, dim3((unsigned)S * kCluster), dim3(kThreads), 0, s, kCluster, a, gp, cp);
+    const int cl = single_cluster(S);
+    e = launch_pdl(lora_single_kernel, dim3((unsigned)(S * (int64_t)cl)), dim3(kSingleThreads), 0, s, cl, a);
   } else {
     const int cl = cluster_size(T, K);
     e = r <= 16 ? launch_tiles<16>(a, cl, s) : r <= 32 ? launch_tiles<32>(a, cl, s)
