@@ -9,9 +9,10 @@
 // products in one launch, so that X A never leaves the chip:
 //   1. X A: each CTA sums its share of K, 64 columns a stage: TMA brings the rows of X and
 //      64 rows of A, tcgen05.mma adds S[128 x RP] in TMEM;
-//   2. the CTAs' partial S are exchanged through distributed shared memory and summed in
-//      rank order; c S is split into two bf16 (its rounding and what the rounding left) and
-//      written as the K-major operand of the second product, K = 2 RP;
+//   2. each CTA receives the partial S of its share of the rows through distributed shared
+//      memory and sums them in rank order; c S is split into two bf16 (its rounding and what
+//      the rounding left) and written as rows of the K-major operand of the second product, K = 2 RP, which bulk
+//      copies bring to the other CTAs;
 //   3. each CTA takes its share of the columns, 64 a stage: TMA brings the rows of Y and 64
 //      columns of B, tcgen05.mma forms S B in TMEM, the epilogue warps add it to Y in
 //      shared memory, and TMA stores the rows back.
@@ -21,7 +22,7 @@
 // bytes over as many SMs.  Only 32-row boxes that hold rows of the request are copied; a box
 // that it shares with another request is stored row by row.
 //
-// lora_single_kernel, for one row per request: a cluster of 8 CTAs per row; see there.
+// lora_single_kernel, for requests of a few rows: a cluster per row, see single_row.
 #include "common.cuh"
 #include "internal.h"
 #include "sequences.cuh"
@@ -46,6 +47,7 @@ struct LoraArgs {
   int n_adapters, K, N, r;
   __nv_bfloat16* Y;
   int64_t ldy;
+  int skip;                // the tiles leave requests of up to this many rows to lora_single_kernel
   int* err;
 };
 
@@ -60,13 +62,17 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
+__device__ __forceinline__ void st_cluster_u4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
                : "memory");
-  return v;
+}
+// Copies this CTA's shared memory to another CTA's (dst and bar as mapa_smem gives them).
+__device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -280,20 +286,30 @@ __device__ __forceinline__ void single_row(const LoraArgs& a, int64_t row, int a
   }
 }
 
-// One row per request (seq_offsets = NULL): a cluster per row.
+// Requests of one row, or of up to kShortRows rows one after the other: a cluster per request.
 constexpr int kSingleThreads = 256;
 __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraArgs a) {
   pdl_begin();
   __shared__ RowSmem<kSingleThreads> sm;
   const int rank = (int)cluster_ctarank(), CL = (int)cluster_nctarank();
-  const int64_t row = (int)blockIdx.x / CL;
-  const int ad = a.adapters[row];
+  const int s = (int)blockIdx.x / CL;
+  int64_t lo = s, hi = s + 1;
+  if (a.off != nullptr) {
+    check_offsets(a.off, a.S, a.T, a.err);
+    lo = a.off[s];
+    hi = a.off[s + 1];
+    if (lo < 0 || hi > a.T || hi <= lo || hi - lo > kShortRows) return;
+  }
+  const int ad = a.adapters[s];
   if (ad < 0) return;                          // (the same for the cluster)
   if (ad >= a.n_adapters) {
     if (threadIdx.x == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
     return;
   }
-  single_row<kSingleThreads>(a, row, ad, rank, CL, 0, sm);
+  for (int64_t t = lo; t < hi; ++t) {
+    if (t > lo) __syncthreads();
+    single_row<kSingleThreads>(a, t, ad, rank, CL, (int)(t - lo), sm);
+  }
 }
 
 // ---------------------------------------------------------------- rows of one adapter
@@ -315,7 +331,6 @@ struct TilesCfg {
   static int smem_bytes(bool cluster) {
     return STAGES * STAGE_BYTES + OP_BYTES + (cluster ? PART_BYTES : 0) + BAR_BYTES + 1024;
   }
-  static_assert(sizeof(RowSmem<THREADS>) <= STAGES * STAGE_BYTES, "short requests use the ring's memory");
   // A chunk [64 K rows][RP], rank innermost: rows of up to 128 bytes, two atoms at rank 128
   static constexpr uint32_t A_SW = RP == 16 ? kSw32 : RP == 32 ? kSw64 : kSw128;
   static constexpr int A_ROWB = (RP < 64 ? RP : 64) * 2;
@@ -335,18 +350,19 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* op = smem + S * C::STAGE_BYTES;                 // [hi | lo] operand of the second product
   uint64_t* bars = reinterpret_cast<uint64_t*>(op + C::OP_BYTES);
-  float* part = reinterpret_cast<float*>(op + C::OP_BYTES + C::BAR_BYTES);   // clusters only
+  float* recv = reinterpret_cast<float*>(op + C::OP_BYTES + C::BAR_BYTES);   // clusters only
   uint64_t* full = bars;                 // [S] TMA bytes of the stage landed
   uint64_t* xfree = bars + S;            // [S] the MMAs of an X stage completed
   uint64_t* yfree = bars + 2 * S;        // [S] a Y stage's rows are stored (4 warps)
   uint64_t* dfull = bars + 3 * S;        // [2] product ready in TMEM
   uint64_t* dfree = bars + 3 * S + 2;    // [2] product read (4 warps)
   uint64_t* acc_done = bars + 3 * S + 4;
-  uint64_t* op_ready = bars + 3 * S + 5;
+  uint64_t* op_ready = bars + 3 * S + 5;     // this CTA's rows of the operand are written
   uint64_t* drain = bars + 3 * S + 6;
-  uint64_t* peer_ready = bars + 3 * S + 7;   // every CTA's partial is written (4 warps each)
-  uint64_t* part_read = bars + 3 * S + 8;    // this CTA's partial is read by every CTA
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 9);
+  uint64_t* recv_ready = bars + 3 * S + 7;   // every CTA's partial of this CTA's rows is here
+  uint64_t* op_full = bars + 3 * S + 8;      // the other CTAs' rows of the operand are here
+  uint64_t* peers_done = bars + 3 * S + 9;   // every CTA has the whole operand
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 10);
 
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
   const int rank = (int)cluster_ctarank(), CL = (int)cluster_nctarank();
@@ -362,9 +378,10 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
     }
     mbar_init(smem_u32(acc_done), 1);
     mbar_init(smem_u32(op_ready), C::BM);
+    mbar_init(smem_u32(op_full), 1);
     mbar_init(smem_u32(drain), 1);
-    mbar_init(smem_u32(peer_ready), 4 * CL);
-    mbar_init(smem_u32(part_read), 4 * CL);
+    mbar_init(smem_u32(recv_ready), 4);
+    mbar_init(smem_u32(peers_done), CL);
     mbar_fence_init();
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmA);
@@ -373,30 +390,14 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
   }
   pdl_begin();
   check_offsets(a.off, a.S, a.T, a.err);
-  // the last S clusters take the short requests, row by row
-  const int slot = (int)blockIdx.x / CL, tiles = (int)gridDim.x / CL - a.S;
-  if (slot >= tiles) {
-    const int64_t lo = a.off[slot - tiles], hi = a.off[slot - tiles + 1];
-    const int ad = a.adapters[slot - tiles];
-    if (hi <= lo || hi - lo > kShortRows || lo < 0 || hi > a.T || ad < 0) return;
-    if (ad >= a.n_adapters) {
-      if (tid == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
-      return;
-    }
-    RowSmem<C::THREADS>& sm = *reinterpret_cast<RowSmem<C::THREADS>*>(smem);
-    for (int64_t t = lo; t < hi; ++t) {
-      if (t > lo) __syncthreads();
-      single_row<C::THREADS>(a, t, ad, rank, CL, (int)(t - lo), sm);
-    }
-    return;
-  }
-  // the others a tile, the same for all CTAs: slot -> (window, request) -> rows, adapter
+  // the cluster's tile, the same for all its CTAs: slot -> (window, request) -> rows, adapter
+  const int slot = (int)blockIdx.x / CL;
   const int s = block_count_le(a.S, slot, [&](int i) { return (long long)a.off[i] / C::BM + i; }) - 1;
   if (s < 0) return;
   const int64_t w = slot - s, lo = a.off[s], hi = a.off[s + 1];
   const int64_t row0 = w * C::BM;
   const int64_t r0 = row0 > lo ? row0 : lo, r1 = row0 + C::BM < hi ? row0 + C::BM : hi;
-  if (lo < 0 || r1 > a.T || r0 >= r1 || hi - lo <= kShortRows) return;
+  if (lo < 0 || r1 > a.T || r0 >= r1 || hi - lo <= a.skip) return;
   const int ad = a.adapters[s];
   if (ad < 0) return;
   if (ad >= a.n_adapters) {
@@ -460,6 +461,11 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t id1 = idesc_bf16(128, RP, 0, 1), id2 = idesc_bf16(128, C::BN, 0, 1);
+      // boxes of the operand's rows that this CTA writes, and how many come from the others
+      const int b0 = rank * 4 / CL, b1 = (rank + 1) * 4 / CL;
+      int theirs = 0;
+      for (int b = box0; b < box1; ++b) theirs += b < b0 || b >= b1 ? 1 : 0;
+      if (theirs > 0) mbar_arrive_expect_tx(smem_u32(op_full), (uint32_t)theirs * 4096 * C::OP_ATOMS);
       for (int it = 0; it < n_x && ok; ++it) {
         const int st = it % S;
         ok = mbar_wait(smem_u32(&full[st]), (it / S) & 1, a.err);
@@ -474,7 +480,22 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
         umma_commit(smem_u32(&xfree[st]));
       }
       umma_commit(smem_u32(acc_done));
-      if (ok && n_y > 0) ok = mbar_wait(smem_u32(op_ready), 0, a.err);
+      if (ok) ok = mbar_wait(smem_u32(op_ready), 0, a.err);
+      if (CL > 1) {
+        // this CTA's rows go to the others as bulk copies, box by box (they pass through the
+        // barriers set up before the partials came)
+        for (int b = box0 > b0 ? box0 : b0; ok && b < (box1 < b1 ? box1 : b1); ++b)
+          for (int q = 0; q < CL; ++q) {
+            if (q == rank) continue;
+            const uint32_t bar = mapa_smem(smem_u32(op_full), (uint32_t)q);
+            for (int x = 0; x < C::OP_ATOMS; ++x) {
+              const uint32_t src = smem_u32(op + x * (C::BM * 128) + b * 4096);
+              bulk_copy_cluster(mapa_smem(src, (uint32_t)q), src, 4096, bar);
+            }
+          }
+        if (ok && theirs > 0) ok = mbar_wait(smem_u32(op_full), 0, a.err);
+        for (int q = 0; q < CL; ++q) mbar_arrive_cluster(mapa_smem(smem_u32(peers_done), (uint32_t)q));
+      }
       tc_fence_after();
       for (int j = 0; j < n_y && ok; ++j) {
         const int it = n_x + j, st = it % S, d = j & 1;
@@ -507,76 +528,77 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
     const float c = a.scale[ad];
-    // partial S in 16-byte pieces, piece g of row t at g ^ (t mod pieces): the rows' banks differ
-    constexpr int PIECES = RP / 4;
-    if (CL > 1) {
+    // c S of a row's eight columns from c0 on, split into two bf16 and written as operand rows
+    const auto write_op = [&](int t, int c0, const float (&x)[8]) {
+      float h[8], l[8];
 #pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = x[i] * c;
+        h[i] = __bfloat162float(__float2bfloat16_rn(v));
+        l[i] = isinf(h[i]) ? 0.f : v - h[i];
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int col = p * RP + c0, chunk = (col % 64) / 8;
+        *reinterpret_cast<uint4*>(op + (col / 64) * (C::BM * 128) + t * 128 + ((chunk ^ (t & 7)) << 4)) =
+            pack8(p == 0 ? h : l);
+      }
+    };
+    if (CL == 1) {
+#pragma unroll 1
       for (int c0 = 0; c0 < RP; c0 += 16) {
         uint32_t v[16];
         tmem_ld16(lanes + c0, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<uint4*>(part + tid * RP + (((c0 / 4 + g) ^ (tid & (PIECES - 1))) * 4)) =
-              make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+        for (int g = 0; g < 2; ++g) {
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * g + i]);
+          write_op(tid, c0 + 8 * g, x);
+        }
       }
-      __syncwarp();
+    } else {
+      // Each CTA owns 128 / CL rows.  Every CTA stores its partial of them in the owner's memory
+      // (row major, 16-byte pieces of row t at piece ^ t, so that rows differ in their banks) ...
+      constexpr int PIECES = RP / 4;
+      const int own = C::BM / CL, owner = warp * CL / 4;
       cluster_wait();                  // (long past: every CTA has set up its barriers)
-      if (lane < CL) mbar_arrive_cluster(mapa_smem(smem_u32(peer_ready), (uint32_t)lane));
-      if (!mbar_wait_cluster(smem_u32(peer_ready), 0, a.err)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-    }
-#pragma unroll 1
-    for (int c0 = 0; c0 < RP; c0 += 16) {
-      float x[16];
-      if (CL > 1) {
+      if (mine) {
+        const uint32_t dst = mapa_smem(smem_u32(recv + (rank * own + tid % own) * RP), (uint32_t)owner);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = 0.f;
-        float4 v[4][4];                // (the loads of all CTAs' partials together)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (q >= CL) break;
-          const uint32_t base = mapa_smem(smem_u32(part + tid * RP), (uint32_t)q);
+        for (int c0 = 0; c0 < RP; c0 += 16) {
+          uint32_t v[16];
+          tmem_ld16(lanes + c0, v);
+          tmem_wait_ld();
 #pragma unroll
           for (int g = 0; g < 4; ++g)
-            v[q][g] = ld_cluster_f4(base + (((c0 / 4 + g) ^ (tid & (PIECES - 1))) * 16));
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (q >= CL) break;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            x[4 * g] += v[q][g].x; x[4 * g + 1] += v[q][g].y;
-            x[4 * g + 2] += v[q][g].z; x[4 * g + 3] += v[q][g].w;
-          }
-        }
-      } else {
-        uint32_t v[16];
-        tmem_ld16(lanes + c0, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
-      }
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float h[8], l[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float v = x[8 * g + i] * c;
-          h[i] = __bfloat162float(__float2bfloat16_rn(v));
-          l[i] = isinf(h[i]) ? 0.f : v - h[i];
-        }
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int col = p * RP + c0 + 8 * g, chunk = (col % 64) / 8;
-          *reinterpret_cast<uint4*>(op + (col / 64) * (C::BM * 128) + tid * 128 + ((chunk ^ (tid & 7)) << 4)) =
-              pack8(p == 0 ? h : l);
+            st_cluster_u4(dst + ((c0 / 4 + g) ^ (tid & (PIECES - 1))) * 16,
+                          make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]));
         }
       }
-    }
-    if (CL > 1) {
       __syncwarp();
-      if (lane < CL) mbar_arrive_cluster(mapa_smem(smem_u32(part_read), (uint32_t)lane));
+      if (lane == 0) mbar_arrive_cluster(mapa_smem(smem_u32(recv_ready), (uint32_t)owner));
+      __syncwarp();
+      // ... and sums what it received for its own rows, in rank order
+      if (!mbar_wait_cluster(smem_u32(recv_ready), 0, a.err)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      for (int i = tid; i < own * (RP / 8); i += C::BM) {
+        const int tl = i % own, g = i / own, t = rank * own + tl;
+        if (t / 32 < box0 || t / 32 >= box1) continue;
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        for (int q = 0; q < CL; ++q) {
+          const float* src = recv + (q * own + tl) * RP;
+          const float4 u = *reinterpret_cast<const float4*>(src + ((2 * g) ^ (t & (PIECES - 1))) * 4);
+          const float4 v = *reinterpret_cast<const float4*>(src + ((2 * g + 1) ^ (t & (PIECES - 1))) * 4);
+          x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
+          x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
+        }
+        write_op(t, 8 * g, x);
+      }
+      __syncwarp();
     }
     tc_fence_before();
     fence_proxy_async_smem();
@@ -636,14 +658,15 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
         }
         if (lane == 0) mbar_arrive(smem_u32(&yfree[st]));
       }
+      __syncwarp();                      // (the TMEM loads that follow are for whole warps)
     }
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
   }
-  // the CTA may go once the others have read its partial
+  // the CTA may go once its copies have reached all the others
   if (CL > 1) {
     if (warp >= 4) cluster_wait();
-    mbar_wait_cluster(smem_u32(part_read), 0, a.err);
+    mbar_wait_cluster(smem_u32(peers_done), 0, a.err);
   }
   tc_fence_before();
   __syncthreads();
@@ -671,19 +694,19 @@ cudaError_t launch_tiles(const LoraArgs& a, int CL, cudaStream_t s) {
   auto kern = lora_tiles_kernel<C>;
   cudaError_t st = ensure_smem(kern, C::smem_bytes(true));
   if (st != cudaSuccess) return st;
-  const int64_t slots = (a.T + C::BM - 1) / C::BM + a.S - 1 + a.S;
+  const int64_t slots = (a.T + C::BM - 1) / C::BM + a.S - 1;
   ProfScope ps(K_LORA_REQUESTS, s);
   return launch_pdl(kern, dim3((unsigned)(slots * CL)), dim3(C::THREADS), smem, s, CL, tx, ta, tb, ty, a);
 }
 
-// CTAs per cluster: as many as keep the windows' clusters within two CTAs per SM (the occupancy
-// up to rank 32), no more than there are 64-column stages of K to share, and at most 4: clusters
-// of 8 find few places (15 at a time on 148 SMs; 4133 rows at 2880 x 2880, rank 16: 78 us with 8,
-// 32 us with 4, 43 us with 2).
-int cluster_size(int64_t T, int K) {
-  const int64_t tiles = (T + 127) / 128;
+// CTAs per cluster: as many as keep the windows' clusters within the CTAs that run at once (two
+// per SM up to rank 32, one above), no more than there are 64-column stages of K to share, and at
+// most 4: clusters of 8 find few places (15 at a time on 148 SMs; 4133 rows at 2880 x 2880, rank
+// 16: 78 us with 8, 32 us with 4, 43 us with 2).
+int cluster_size(int64_t T, int K, int r) {
+  const int64_t tiles = (T + 127) / 128, room = (int64_t)device_sms() * (r <= 32 ? 2 : 1);
   int cl = 1;
-  while (cl < 4 && tiles * cl * 2 <= 2 * (int64_t)device_sms() && cl * 2 <= (K + 63) / 64) cl *= 2;
+  while (cl < 4 && tiles * cl * 2 <= room && cl * 2 <= (K + 63) / 64) cl *= 2;
   return cl;
 }
 
@@ -735,13 +758,17 @@ extern "C" moe_status_t moe_lora_requests(const moe_bf16_t* X, int64_t ldx, cons
   a.err = moe_status_word();
   if (a.err == nullptr) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (seq_offsets == nullptr) {
+  // Short requests row by row where there are several (a row takes 5 us there and 19 us as a
+  // tile, which beats a launch of its own for a few).
+  cudaError_t e = cudaSuccess;
+  if (seq_offsets == nullptr || S >= 8 || T <= kShortRows) {
     ProfScope ps(K_LORA_REQUESTS, s);
     const int cl = single_cluster(S);
     e = launch_pdl(lora_single_kernel, dim3((unsigned)(S * (int64_t)cl)), dim3(kSingleThreads), 0, s, cl, a);
-  } else {
-    const int cl = cluster_size(T, K);
+    a.skip = kShortRows;
+  }
+  if (e == cudaSuccess && seq_offsets != nullptr && T > a.skip) {
+    const int cl = cluster_size(T, K, r);
     e = r <= 16 ? launch_tiles<16>(a, cl, s) : r <= 32 ? launch_tiles<32>(a, cl, s)
         : r <= 64 ? launch_tiles<64>(a, cl, s) : launch_tiles<128>(a, cl, s);
   }
