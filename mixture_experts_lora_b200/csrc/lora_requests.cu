@@ -23,6 +23,8 @@
 // that it shares with another request is stored row by row.
 //
 // lora_single_kernel, for requests of a few rows: a cluster per row, see single_row.
+#include <climits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "sequences.cuh"
@@ -116,7 +118,7 @@ template <int NT>
 struct RowSmem {
   float x[kXChunk];
   float warp[NT / 32][128];
-  float part[2][kMaxCluster][128];    // every CTA's sum over its share of K, rows in turn
+  float part[kMaxCluster][128];       // every CTA's sum over its share of K
   float xa[128];
   float4 out[2][NT];                  // partial sums of eight columns
 };
@@ -136,7 +138,7 @@ __device__ __forceinline__ void add_scaled(float (&y)[8], uint4 w, float x) {
 }
 
 template <int NT>
-__device__ __forceinline__ void single_row(const LoraArgs& a, int64_t row, int ad, int rank, int CL, int turn,
+__device__ __forceinline__ void single_row(const LoraArgs& a, int64_t row, int ad, int rank, int CL,
                                            RowSmem<NT>& sm) {
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
   const float scale = a.scale[ad];
@@ -223,7 +225,7 @@ __device__ __forceinline__ void single_row(const LoraArgs& a, int64_t row, int a
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < NT / 32; ++i) v += sm.warp[i][tid];
-    const uint32_t mine = smem_u32(&sm.part[turn & 1][rank][tid]);
+    const uint32_t mine = smem_u32(&sm.part[rank][tid]);
     for (int q = 0; q < CL; ++q) st_cluster_f32(mapa_smem(mine, (uint32_t)q), v);
   }
   // the eight elements of Y that this thread finishes in a pass
@@ -234,7 +236,7 @@ __device__ __forceinline__ void single_row(const LoraArgs& a, int64_t row, int a
   cluster_sync();
   if (tid < a.r) {
     float v = 0.f;
-    for (int i = 0; i < CL; ++i) v += sm.part[turn & 1][i][tid];
+    for (int i = 0; i < CL; ++i) v += sm.part[i][tid];
     sm.xa[tid] = v * scale;
   }
   __syncthreads();
@@ -286,30 +288,27 @@ __device__ __forceinline__ void single_row(const LoraArgs& a, int64_t row, int a
   }
 }
 
-// Requests of one row, or of up to kShortRows rows one after the other: a cluster per request.
+// Requests of one row (a cluster each), or of up to kShortRows rows (a cluster per row).
 constexpr int kSingleThreads = 256;
 __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraArgs a) {
   pdl_begin();
   __shared__ RowSmem<kSingleThreads> sm;
   const int rank = (int)cluster_ctarank(), CL = (int)cluster_nctarank();
-  const int s = (int)blockIdx.x / CL;
-  int64_t lo = s, hi = s + 1;
-  if (a.off != nullptr) {
-    check_offsets(a.off, a.S, a.T, a.err);
-    lo = a.off[s];
-    hi = a.off[s + 1];
-    if (lo < 0 || hi > a.T || hi <= lo || hi - lo > kShortRows) return;
-  }
+  const int slot = (int)blockIdx.x / CL, s = a.off == nullptr ? slot : slot / kShortRows;
   const int ad = a.adapters[s];
+  int64_t row = slot;
+  if (a.off != nullptr) {
+    const int64_t lo = a.off[s], hi = a.off[s + 1];
+    check_offsets(a.off, a.S, a.T, a.err);
+    row = lo + slot % kShortRows;
+    if (lo < 0 || hi > a.T || row >= hi || hi - lo > kShortRows) return;
+  }
   if (ad < 0) return;                          // (the same for the cluster)
   if (ad >= a.n_adapters) {
     if (threadIdx.x == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
     return;
   }
-  for (int64_t t = lo; t < hi; ++t) {
-    if (t > lo) __syncthreads();
-    single_row<kSingleThreads>(a, t, ad, rank, CL, (int)(t - lo), sm);
-  }
+  single_row<kSingleThreads>(a, row, ad, rank, CL, sm);
 }
 
 // ---------------------------------------------------------------- rows of one adapter
@@ -392,14 +391,36 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
   check_offsets(a.off, a.S, a.T, a.err);
   // the cluster's tile, the same for all its CTAs: slot -> (window, request) -> rows, adapter
   const int slot = (int)blockIdx.x / CL;
-  const int s = block_count_le(a.S, slot, [&](int i) { return (long long)a.off[i] / C::BM + i; }) - 1;
-  if (s < 0) return;
-  const int64_t w = slot - s, lo = a.off[s], hi = a.off[s + 1];
+  int s, ad;
+  int64_t lo, hi;
+  if (a.S <= C::THREADS) {
+    // a thread per request: one of them finds the slot among its own (one wait for memory)
+    __shared__ int found[4];
+    if (tid == 0) found[0] = -1;
+    int f0 = 0, f1 = 0, o0 = 0, o1 = 0, my_ad = 0;
+    if (tid < a.S) {
+      o0 = a.off[tid];
+      o1 = a.off[tid + 1];
+      my_ad = a.adapters[tid];
+      f0 = o0 / C::BM + tid;
+      f1 = tid + 1 < a.S ? o1 / C::BM + tid + 1 : INT_MAX;
+    }
+    __syncthreads();
+    if (tid < a.S && f0 <= slot && slot < f1) {
+      found[0] = tid; found[1] = o0; found[2] = o1; found[3] = my_ad;
+    }
+    __syncthreads();
+    s = found[0]; lo = found[1]; hi = found[2]; ad = found[3];
+    if (s < 0) return;
+  } else {
+    s = block_count_le(a.S, slot, [&](int i) { return (long long)a.off[i] / C::BM + i; }) - 1;
+    if (s < 0) return;
+    lo = a.off[s]; hi = a.off[s + 1]; ad = a.adapters[s];
+  }
+  const int64_t w = slot - s;
   const int64_t row0 = w * C::BM;
   const int64_t r0 = row0 > lo ? row0 : lo, r1 = row0 + C::BM < hi ? row0 + C::BM : hi;
-  if (lo < 0 || r1 > a.T || r0 >= r1 || hi - lo <= a.skip) return;
-  const int ad = a.adapters[s];
-  if (ad < 0) return;
+  if (lo < 0 || r1 > a.T || r0 >= r1 || hi - lo <= a.skip || ad < 0) return;
   if (ad >= a.n_adapters) {
     if (tid == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
     return;
@@ -639,8 +660,13 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
           mbar_arrive(smem_u32(&dfree[d]));
           tma_store_2d(&tmY, smem_u32(rows + warp * 4096), n0, (int)brow);
           bulk_commit_group();
-          bulk_wait_read<0>();
-          mbar_arrive(smem_u32(&yfree[st]));
+          if constexpr (S >= 4) {        // the stage before is read by now, or nearly
+            bulk_wait_read<1>();
+            if (j > 0) mbar_arrive(smem_u32(&yfree[(it - 1) % S]));
+          } else {                       // (three slots: none to spare for that)
+            bulk_wait_read<0>();
+            mbar_arrive(smem_u32(&yfree[st]));
+          }
         }
       } else {
         __syncwarp();
@@ -758,13 +784,14 @@ extern "C" moe_status_t moe_lora_requests(const moe_bf16_t* X, int64_t ldx, cons
   a.err = moe_status_word();
   if (a.err == nullptr) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Short requests row by row where there are several (a row takes 5 us there and 19 us as a
-  // tile, which beats a launch of its own for a few).
+  // Short requests row by row where there can be many of them: the launch costs a batch without
+  // any 5 us, a tile takes 16 us however few its rows, and tiles find room for a few more.
   cudaError_t e = cudaSuccess;
-  if (seq_offsets == nullptr || S >= 8 || T <= kShortRows) {
+  if (seq_offsets == nullptr || (S >= 8 && T <= (int64_t)256 * S) || T <= kShortRows) {
     ProfScope ps(K_LORA_REQUESTS, s);
+    const int64_t rows = seq_offsets == nullptr ? S : (int64_t)S * kShortRows;
     const int cl = single_cluster(S);
-    e = launch_pdl(lora_single_kernel, dim3((unsigned)(S * (int64_t)cl)), dim3(kSingleThreads), 0, s, cl, a);
+    e = launch_pdl(lora_single_kernel, dim3((unsigned)(rows * cl)), dim3(kSingleThreads), 0, s, cl, a);
     a.skip = kShortRows;
   }
   if (e == cudaSuccess && seq_offsets != nullptr && T > a.skip) {
