@@ -326,7 +326,10 @@ struct TilesCfg {
   static constexpr int PART_BYTES = BM * RP * 4;          // exchanged partial (clusters only)
   static constexpr int BAR_BYTES = 256;
   static constexpr int TMEM_COLS = 128;                   // two 64-column accumulators; S before them
-  static constexpr int THREADS = 192;                     // epilogue warps 0-3, loader, MMA issuer
+  // two groups of four epilogue warps (the second stage by stage in turn with the first), loader,
+  // MMA issuer
+  static constexpr int THREADS = 320;
+  static constexpr int LOADER = 8, ISSUER = 9;
   static int smem_bytes(bool cluster) {
     return STAGES * STAGE_BYTES + OP_BYTES + (cluster ? PART_BYTES : 0) + BAR_BYTES + 1024;
   }
@@ -337,8 +340,7 @@ struct TilesCfg {
   static constexpr int A_ATOM_BYTES = BK * A_ROWB;
 };
 
-// (Registers are given to warps in fours, so two blocks of six warps hold as many as two of
-// eight: at most 128 a thread.)
+// (Registers are given to warps in fours: two blocks of ten warps hold as many as two of twelve.)
 template <class C>
 __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
     lora_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
   const int n_x = (nk - rank + CL - 1) / CL;      // this CTA's stages: rank, rank + CL, ...
   const int n_y = rank < nn ? (nn - rank + CL - 1) / CL : 0;
 
-  if (warp == 5) {
+  if (warp == C::ISSUER) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
   bool ok = true;
   if (CL > 1) cluster_arrive();        // this CTA's barriers are there for the others' arrivals
 
-  if (warp == 4) {
+  if (warp == C::LOADER) {
     // ------------------------------------------------------------ loader
     if (lane == 0) {
       const uint32_t bytes = (uint32_t)(box1 - box0) * 32 * 128 + C::AD_BYTES;
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
       for (int j = it < S ? 0 : it - S; !ok && j < it; ++j) mbar_wait(smem_u32(&full[j % S]), (j / S) & 1, a.err);
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == C::ISSUER) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t id1 = idesc_bf16(128, RP, 0, 1), id2 = idesc_bf16(128, C::BN, 0, 1);
@@ -542,91 +544,94 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ epilogue warps: tile row = tid
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    const bool mine = warp >= box0 && warp < box1;         // this warp's box holds rows
-    ok = mbar_wait(smem_u32(acc_done), 0, a.err);
-    ok = __all_sync(0xffffffffu, ok);
-    tc_fence_after();
-    const float c = a.scale[ad];
-    // c S of a row's eight columns from c0 on, split into two bf16 and written as operand rows
-    const auto write_op = [&](int t, int c0, const float (&x)[8]) {
-      float h[8], l[8];
+    // ------------------------------------------------------------ epilogue warps: tile row = tid % 128
+    const int group = warp / 4, quarter = warp % 4, trow = tid % C::BM;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const bool mine = quarter >= box0 && quarter < box1;   // this warp's box holds rows
+    if (group == 0) {
+      ok = mbar_wait(smem_u32(acc_done), 0, a.err);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      const float c = a.scale[ad];
+      // c S of a row's eight columns from c0 on, split into two bf16 and written as operand rows
+      const auto write_op = [&](int t, int c0, const float (&x)[8]) {
+        float h[8], l[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = x[i] * c;
-        h[i] = __bfloat162float(__float2bfloat16_rn(v));
-        l[i] = isinf(h[i]) ? 0.f : v - h[i];
-      }
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int col = p * RP + c0, chunk = (col % 64) / 8;
-        *reinterpret_cast<uint4*>(op + (col / 64) * (C::BM * 128) + t * 128 + ((chunk ^ (t & 7)) << 4)) =
-            pack8(p == 0 ? h : l);
-      }
-    };
-    if (CL == 1) {
-#pragma unroll 1
-      for (int c0 = 0; c0 < RP; c0 += 16) {
-        uint32_t v[16];
-        tmem_ld16(lanes + c0, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * g + i]);
-          write_op(tid, c0 + 8 * g, x);
+        for (int i = 0; i < 8; ++i) {
+          const float v = x[i] * c;
+          h[i] = __bfloat162float(__float2bfloat16_rn(v));
+          l[i] = isinf(h[i]) ? 0.f : v - h[i];
         }
-      }
-    } else {
-      // Each CTA owns 128 / CL rows.  Every CTA stores its partial of them in the owner's memory
-      // (row major, 16-byte pieces of row t at piece ^ t, so that rows differ in their banks) ...
-      constexpr int PIECES = RP / 4;
-      const int own = C::BM / CL, owner = warp * CL / 4;
-      cluster_wait();                  // (long past: every CTA has set up its barriers)
-      if (mine) {
-        const uint32_t dst = mapa_smem(smem_u32(recv + (rank * own + tid % own) * RP), (uint32_t)owner);
 #pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int col = p * RP + c0, chunk = (col % 64) / 8;
+          *reinterpret_cast<uint4*>(op + (col / 64) * (C::BM * 128) + t * 128 + ((chunk ^ (t & 7)) << 4)) =
+              pack8(p == 0 ? h : l);
+        }
+      };
+      if (CL == 1) {
+#pragma unroll 1
         for (int c0 = 0; c0 < RP; c0 += 16) {
           uint32_t v[16];
           tmem_ld16(lanes + c0, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            st_cluster_u4(dst + ((c0 / 4 + g) ^ (tid & (PIECES - 1))) * 16,
-                          make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]));
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_smem(smem_u32(recv_ready), (uint32_t)owner));
-      __syncwarp();
-      // ... and sums what it received for its own rows, in rank order
-      if (!mbar_wait_cluster(smem_u32(recv_ready), 0, a.err)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-      for (int i = tid; i < own * (RP / 8); i += C::BM) {
-        const int tl = i % own, g = i / own, t = rank * own + tl;
-        if (t / 32 < box0 || t / 32 >= box1) continue;
-        float x[8];
+          for (int g = 0; g < 2; ++g) {
+            float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        for (int q = 0; q < CL; ++q) {
-          const float* src = recv + (q * own + tl) * RP;
-          const float4 u = *reinterpret_cast<const float4*>(src + ((2 * g) ^ (t & (PIECES - 1))) * 4);
-          const float4 v = *reinterpret_cast<const float4*>(src + ((2 * g + 1) ^ (t & (PIECES - 1))) * 4);
-          x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
-          x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * g + i]);
+            write_op(tid, c0 + 8 * g, x);
+          }
         }
-        write_op(t, 8 * g, x);
+      } else {
+        // Each CTA owns 128 / CL rows.  Every CTA stores its partial of them in the owner's memory
+        // (row major, 16-byte pieces of row t at piece ^ t, so that rows differ in their banks) ...
+        constexpr int PIECES = RP / 4;
+        const int own = C::BM / CL, owner = warp * CL / 4;
+        cluster_wait();                  // (long past: every CTA has set up its barriers)
+        if (mine) {
+          const uint32_t dst = mapa_smem(smem_u32(recv + (rank * own + tid % own) * RP), (uint32_t)owner);
+#pragma unroll
+          for (int c0 = 0; c0 < RP; c0 += 16) {
+            uint32_t v[16];
+            tmem_ld16(lanes + c0, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              st_cluster_u4(dst + ((c0 / 4 + g) ^ (tid & (PIECES - 1))) * 16,
+                            make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]));
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_smem(smem_u32(recv_ready), (uint32_t)owner));
+        __syncwarp();
+        // ... and sums what it received for its own rows, in rank order
+        if (!mbar_wait_cluster(smem_u32(recv_ready), 0, a.err)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        for (int i = tid; i < own * (RP / 8); i += C::BM) {
+          const int tl = i % own, g = i / own, t = rank * own + tl;
+          if (t / 32 < box0 || t / 32 >= box1) continue;
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = 0.f;
+          for (int q = 0; q < CL; ++q) {
+            const float* src = recv + (q * own + tl) * RP;
+            const float4 u = *reinterpret_cast<const float4*>(src + ((2 * g) ^ (t & (PIECES - 1))) * 4);
+            const float4 v = *reinterpret_cast<const float4*>(src + ((2 * g + 1) ^ (t & (PIECES - 1))) * 4);
+            x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
+            x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
+          }
+          write_op(t, 8 * g, x);
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      tc_fence_before();
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(op_ready));
     }
-    tc_fence_before();
-    fence_proxy_async_smem();
-    mbar_arrive(smem_u32(op_ready));
-    const int64_t brow = row0 + warp * 32;                 // first row of this warp's box
+    const int64_t brow = row0 + quarter * 32;              // first row of this warp's box
     const bool whole = mine && brow >= r0 && brow + 32 <= r1;
-    for (int j = 0; j < n_y; ++j) {
+    for (int j = group; j < n_y; j += 2) {
       const int it = n_x + j, st = it % S, d = j & 1;
       if (ok) ok = mbar_wait(smem_u32(&dfull[d]), (j / 2) & 1, a.err);
       if (ok) ok = mbar_wait(smem_u32(&full[st]), (it / S) & 1, a.err);
@@ -643,7 +648,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
           tmem_wait_ld();
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            uint4* p = reinterpret_cast<uint4*>(rows + tid * 128 + (((half * 4 + g) ^ (tid & 7)) << 4));
+            uint4* p = reinterpret_cast<uint4*>(rows + trow * 128 + (((half * 4 + g) ^ (trow & 7)) << 4));
             float y[8];
             unpack8(*p, y);
 #pragma unroll
@@ -658,15 +663,10 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&dfree[d]));
-          tma_store_2d(&tmY, smem_u32(rows + warp * 4096), n0, (int)brow);
+          tma_store_2d(&tmY, smem_u32(rows + quarter * 4096), n0, (int)brow);
           bulk_commit_group();
-          if constexpr (S >= 4) {        // the stage before is read by now, or nearly
-            bulk_wait_read<1>();
-            if (j > 0) mbar_arrive(smem_u32(&yfree[(it - 1) % S]));
-          } else {                       // (three slots: none to spare for that)
-            bulk_wait_read<0>();
-            mbar_arrive(smem_u32(&yfree[st]));
-          }
+          bulk_wait_read<0>();
+          mbar_arrive(smem_u32(&yfree[st]));
         }
       } else {
         __syncwarp();
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
         if (mine) {
           // four rows at a time, eight lanes a row
           for (int i = 0; i < 32; i += 4) {
-            const int t = warp * 32 + i + lane / 8, g = lane & 7, n = n0 + g * 8;
+            const int t = quarter * 32 + i + lane / 8, g = lane & 7, n = n0 + g * 8;
             const int64_t row = row0 + t;
             if (row >= r0 && row < r1 && n < a.N)
               *reinterpret_cast<uint4*>(a.Y + row * a.ldy + n) =
@@ -691,12 +691,12 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
   }
   // the CTA may go once its copies have reached all the others
   if (CL > 1) {
-    if (warp >= 4) cluster_wait();
+    if (warp >= 4) cluster_wait();       // (those that did not exchange)
     mbar_wait_cluster(smem_u32(peers_done), 0, a.err);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == C::ISSUER) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
