@@ -24,6 +24,7 @@
 //
 // lora_single_kernel, for requests of a few rows: a cluster per row, see single_row.
 #include <climits>
+#include <cmath>
 
 #include "common.cuh"
 #include "internal.h"
@@ -725,15 +726,28 @@ cudaError_t launch_tiles(const LoraArgs& a, int CL, cudaStream_t s) {
   return launch_pdl(kern, dim3((unsigned)(slots * CL)), dim3(C::THREADS), smem, s, CL, tx, ta, tb, ty, a);
 }
 
-// CTAs per cluster: as many as keep the windows' clusters within the CTAs that run at once (two
-// per SM up to rank 32, one above), no more than there are 64-column stages of K to share, and at
-// most 4: clusters of 8 find few places (15 at a time on 148 SMs; 4133 rows at 2880 x 2880, rank
-// 16: 78 us with 8, 32 us with 4, 43 us with 2).
-int cluster_size(int64_t T, int K, int r) {
-  const int64_t tiles = (T + 127) / 128, room = (int64_t)device_sms() * (r <= 32 ? 2 : 1);
-  int cl = 1;
-  while (cl < 4 && tiles * cl * 2 <= room && cl * 2 <= (K + 63) / 64) cl *= 2;
-  return cl;
+// CTAs per cluster, 1, 2 or 4: what finishes the tiles soonest if a tile takes 1 / CL and the
+// clusters that run at once are as many as measured: two CTAs per SM up to rank 32, one above, and
+// for clusters of four 33 times four CTAs on 148 SMs (clusters of 8, 15 times eight, always lost).
+// Where one CTA runs per SM a last wave of a few clusters costs as much as a full one (rank 64,
+// 35 tiles at 7168 x 4096: 58 us with 2, 65 us with 4, 101 us with 1); two per SM fill it up (rank
+// 16, 67 tiles at 2048 x 2048: 27.9 us with 4, 30.1 us with 2, 42.6 us with 1).
+int cluster_size(int64_t T, int S, int K, int r) {
+  const double windows = (double)((T + 127) / 128);
+  const double tiles = windows + (S - 1 < windows / 2 ? S - 1 : windows / 2);   // requests cut windows
+  const int per_sm = r <= 32 ? 2 : 1;
+  int best = 1;
+  double most = 0.;
+  for (int cl = 1; cl <= 4 && cl <= (K + 63) / 64; cl *= 2) {
+    const double room = device_sms() * (cl < 4 ? 1. / cl : 2. / 9.) * per_sm;
+    double waves = tiles / room;
+    waves = waves < 1. ? 1. : per_sm == 1 ? std::ceil(waves) : waves;
+    if (cl / waves > most * 1.1) {           // (a cluster has its own cost)
+      most = cl / waves;
+      best = cl;
+    }
+  }
+  return best;
 }
 
 // CTAs per row of lora_single_kernel: 8 while all clusters find a place at once (15 of 8 CTAs),
@@ -795,7 +809,7 @@ extern "C" moe_status_t moe_lora_requests(const moe_bf16_t* X, int64_t ldx, cons
     a.skip = kShortRows;
   }
   if (e == cudaSuccess && seq_offsets != nullptr && T > a.skip) {
-    const int cl = cluster_size(T, K, r);
+    const int cl = cluster_size(T, S, K, r);
     e = r <= 16 ? launch_tiles<16>(a, cl, s) : r <= 32 ? launch_tiles<32>(a, cl, s)
         : r <= 64 ? launch_tiles<64>(a, cl, s) : launch_tiles<128>(a, cl, s);
   }
