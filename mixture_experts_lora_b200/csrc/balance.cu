@@ -43,6 +43,7 @@ struct BalanceArgs {
   int32_t* out_counts;
   int32_t* out_n;
   int lanes;               // lanes per row
+  int sum_ranks;           // blocks per sequence of balance_sum_kernel
   int* err;
   // backward
   const int32_t* counts;
@@ -279,17 +280,18 @@ __global__ void __launch_bounds__(kThreads, C::N <= 8 ? 4 : 2) balance_partial_k
   }
 }
 
-// One block per sequence: its partial rows summed in window order (a warp every warps-th
-// window, then the warps in order).
+// A cluster per sequence: its partial rows summed in window order (a warp every warps-th window,
+// then the warps in order).  Block b of the cluster sums every cluster-th group of 32 experts;
+// block 0 adds the blocks' parts of the loss in order.
 constexpr int kSumThreads = 1024;
 __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceArgs a) {
-  const int warps = (int)blockDim.x / 32;
   pdl_begin();
-  __shared__ float s_sum[32][128];
-  __shared__ int s_cnt[32][128];
-  __shared__ float s_part[32];
+  __shared__ float s_sum[32][33];
+  __shared__ int s_cnt[32][33];
+  __shared__ float s_part[32], s_loss[8];
   __shared__ int s_n;
-  const int s = blockIdx.x, E = a.E, warp = warp_id(), lane = lane_id();
+  const int warps = (int)blockDim.x / 32, warp = warp_id(), lane = lane_id(), E = a.E;
+  const int rank = (int)cluster_ctarank(), ranks = a.sum_ranks, s = (int)blockIdx.x / ranks;
   const int64_t n_win = (a.T + a.rows - 1) / a.rows;
   const int64_t r0 = a.off != nullptr ? a.off[s] : 0, r1 = a.off != nullptr ? a.off[s + 1] : a.T;
   // first and last window of the sequence (none if it is empty), within the table whatever
@@ -306,41 +308,62 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceA
   for (int64_t w = w0 + threadIdx.x; w < w1; w += blockDim.x) n += a.pn[w + s];
   if (n != 0) atomicAdd(&s_n, n);
   float part = 0.f;
-  for (int e0 = 0; e0 < E; e0 += 128) {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    int cnt[4] = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int64_t w = w0 + warp; w < w1; w += warps) {
+  for (int e0 = rank * 32; e0 < E; e0 += ranks * 32) {
+    const int e = e0 + lane;
+    float sum = 0.f;
+    int cnt = 0;
+    if (e < E) {
+      const float* ps = a.psum + s * (int64_t)E + e;
+      const int32_t* pc = a.pcnt + s * (int64_t)E + e;
+      int64_t w = w0 + warp;
+      for (; w + 3 * warps < w1; w += 4 * warps) {       // four loads of each on their way
+        float v[4];
+        int c[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = e0 + i * 32 + lane;
-        if (e < E) {
-          sum[i] += a.psum[(w + s) * E + e];
-          cnt[i] += a.pcnt[(w + s) * E + e];
+        for (int i = 0; i < 4; ++i) {
+          v[i] = ps[(w + i * warps) * E];
+          c[i] = pc[(w + i * warps) * E];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum += v[i];
+          cnt += c[i];
         }
       }
+      for (; w < w1; w += warps) {
+        sum += ps[w * E];
+        cnt += pc[w * E];
+      }
     }
+    __syncthreads();                                     // the last group's sums are read
+    s_sum[warp][lane] = sum;
+    s_cnt[warp][lane] = cnt;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s_sum[warp][i * 32 + lane] = sum[i];
-      s_cnt[warp][i * 32 + lane] = cnt[i];
-    }
-    __syncthreads();
-    const int e = e0 + threadIdx.x;
-    if (threadIdx.x < 128 && e < E) {
+    if (warp == 0 && e < E) {
       float v = 0.f;
       int c = 0;
       for (int i = 0; i < warps; ++i) {
-        v += s_sum[i][threadIdx.x];
-        c += s_cnt[i][threadIdx.x];
+        v += s_sum[i][lane];
+        c += s_cnt[i][lane];
       }
       a.out_counts[(int64_t)s * E + e] = c;
       part += (float)c * v;
     }
   }
-  const float all = block_sum(part, s_part);
-  if (threadIdx.x == 0) {
+  const float mine = block_sum(part, s_part);
+  if (ranks > 1) {
+    if (threadIdx.x == 0) {
+      const uint32_t dst = mapa_smem(smem_u32(&s_loss[rank]), 0u);
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(mine) : "memory");
+    }
+    cluster_sync();
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    float all = mine;
+    if (ranks > 1) {
+      all = 0.f;
+      for (int i = 0; i < ranks; ++i) all += s_loss[i];
+    }
     a.loss[s] = all * loss_factor(E, a.k, s_n);
     a.out_n[s] = s_n;
   }
@@ -479,14 +502,15 @@ cudaError_t launch_rows(BalanceArgs& a, int64_t n_win, cudaStream_t s) {
 }
 
 // Rows per window.  Batches of up to 32768 logits in few sequences: one window, which needs no
-// second launch.  Otherwise at most about four windows per SM, so that a sequence's partial rows
-// stay few, and 32 rows at least, less where sequences are shorter (a window works through its
-// sequences one after the other).
+// second launch.  Otherwise about four windows per SM, two above 256 experts (a block writes, and
+// the second launch reads, a partial row per window), and 32 rows at least, less where sequences
+// are shorter (a window works through its sequences one after the other).
 int window_rows(int64_t T, int E, int S) {
   if (T * E <= 32768 && S <= 4) return T > 0 ? (int)T : 1;
   int64_t low = T / S;
   low = low > 32 ? 32 : low < 8 ? 8 : low;
-  const int64_t per = (T + 591) / 592;
+  const int64_t windows = E <= 256 ? 592 : 296;
+  const int64_t per = (T + windows - 1) / windows;
   return (int)(per < low ? low : per);
 }
 
@@ -563,8 +587,12 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_ids, int6
   if (!one) {
     a.loss = loss;
     ProfScope ps(K_BALANCE_SUM, s);
-    if (launch_pdl(balance_sum_kernel, dim3((unsigned)S),
-                   dim3(L.n_win > 32 * (int64_t)S ? kSumThreads : kThreads), 0, s, 1, a) != cudaSuccess)
+    // many windows per sequence: large blocks, and up to 8 of them where sequences are few
+    const bool many = L.n_win > 32 * (int64_t)S;
+    a.sum_ranks = 1;
+    while (a.sum_ranks < 8 && a.sum_ranks * 32 < E && S * (int64_t)a.sum_ranks < device_sms()) a.sum_ranks *= 2;
+    if (launch_pdl(balance_sum_kernel, dim3((unsigned)S * a.sum_ranks), dim3(many ? kSumThreads : kThreads), 0, s,
+                   a.sum_ranks, a) != cudaSuccess)
       return MOE_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
