@@ -59,18 +59,19 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// How a row lies in a warp: V consecutive experts at a time, NQ times; FULL: over all 32 lanes.
-template <int V_, int NQ_, bool FULL_>
+// How a row lies in a warp: V consecutive experts at a time, NQ times, over LANES lanes (0: as
+// many as the launch says).
+template <int V_, int NQ_, int LANES_>
 struct RowCfg {
-  static constexpr int V = V_, NQ = NQ_, N = V * NQ;
-  static constexpr bool FULL = FULL_;
+  static constexpr int V = V_, NQ = NQ_, N = V * NQ, LANES = LANES_;
+  static constexpr bool FULL = LANES == 32;
   static constexpr int U = N <= 4 ? 4 : N <= 8 ? 2 : 1;      // rows loaded at once
 };
 
 // The lanes of a row.
 struct Lanes {
   int L, sub, group, groups;     // lanes per row, lane within its row, row within the warp, rows
-  __device__ __forceinline__ Lanes(bool full, int l) : L(full ? 32 : l) {
+  __device__ __forceinline__ Lanes(int fixed, int l) : L(fixed != 0 ? fixed : l) {
     sub = lane_id() & (L - 1);
     groups = 32 / L;
     group = lane_id() / L;
@@ -83,14 +84,23 @@ __device__ __forceinline__ float row_max(float v, const Lanes& ln) {
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
   } else {
-    for (int o = ln.L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if constexpr (C::LANES != 0) {
+#pragma unroll
+      for (int o = C::LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    } else {
+      for (int o = ln.L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    }
     return v;
   }
 }
 template <class C>
 __device__ __forceinline__ float row_sum(float v, const Lanes& ln) {
-  if constexpr (C::FULL) return warp_sum(v);
-  for (int o = ln.L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (C::LANES != 0) {
+#pragma unroll
+    for (int o = C::LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  } else {
+    for (int o = ln.L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  }
   return v;
 }
 
@@ -169,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, C::N <= 8 ? 4 : 2) balance_partial_k
   __shared__ int s_n;
   __shared__ float s_part[kWarps];
   const int warp = warp_id(), E = a.E;
-  const Lanes ln(C::FULL, a.lanes);
+  const Lanes ln(C::LANES, a.lanes);
   const int64_t w = blockIdx.x, t0 = w * a.rows;
   const int64_t t1 = t0 + a.rows < a.T ? t0 + a.rows : a.T;
   int s = 0;
@@ -373,7 +383,7 @@ template <class C>
 __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const BalanceArgs a) {
   pdl_begin();
   const int warp = warp_id(), E = a.E;
-  const Lanes ln(C::FULL, a.lanes);
+  const Lanes ln(C::LANES, a.lanes);
   const int64_t t0 = (int64_t)blockIdx.x * a.rows;
   const int64_t t1 = t0 + a.rows < a.T ? t0 + a.rows : a.T;
   int s = 0;
@@ -486,19 +496,21 @@ cudaError_t launch_rows(BalanceArgs& a, int64_t n_win, cudaStream_t s) {
   while (a.lanes < 32 && a.lanes < groups) a.lanes *= 2;
   const int nq = (groups + a.lanes - 1) / a.lanes;
   if (v4) {
-    if (a.lanes < 32) return K::template launch<RowCfg<4, 1, false>>(a, n_win, s);
-    if (nq <= 1) return K::template launch<RowCfg<4, 1, true>>(a, n_win, s);
-    if (nq <= 2) return K::template launch<RowCfg<4, 2, true>>(a, n_win, s);
-    if (nq <= 4) return K::template launch<RowCfg<4, 4, true>>(a, n_win, s);
-    return K::template launch<RowCfg<4, 8, true>>(a, n_win, s);
+    if (a.lanes == 16) return K::template launch<RowCfg<4, 1, 16>>(a, n_win, s);
+    if (a.lanes == 8) return K::template launch<RowCfg<4, 1, 8>>(a, n_win, s);
+    if (a.lanes < 32) return K::template launch<RowCfg<4, 1, 0>>(a, n_win, s);
+    if (nq <= 1) return K::template launch<RowCfg<4, 1, 32>>(a, n_win, s);
+    if (nq <= 2) return K::template launch<RowCfg<4, 2, 32>>(a, n_win, s);
+    if (nq <= 4) return K::template launch<RowCfg<4, 4, 32>>(a, n_win, s);
+    return K::template launch<RowCfg<4, 8, 32>>(a, n_win, s);
   }
-  if (a.lanes < 32) return K::template launch<RowCfg<1, 1, false>>(a, n_win, s);
-  if (nq <= 1) return K::template launch<RowCfg<1, 1, true>>(a, n_win, s);
-  if (nq <= 2) return K::template launch<RowCfg<1, 2, true>>(a, n_win, s);
-  if (nq <= 4) return K::template launch<RowCfg<1, 4, true>>(a, n_win, s);
-  if (nq <= 8) return K::template launch<RowCfg<1, 8, true>>(a, n_win, s);
-  if (nq <= 16) return K::template launch<RowCfg<1, 16, true>>(a, n_win, s);
-  return K::template launch<RowCfg<1, 32, true>>(a, n_win, s);
+  if (a.lanes < 32) return K::template launch<RowCfg<1, 1, 0>>(a, n_win, s);
+  if (nq <= 1) return K::template launch<RowCfg<1, 1, 32>>(a, n_win, s);
+  if (nq <= 2) return K::template launch<RowCfg<1, 2, 32>>(a, n_win, s);
+  if (nq <= 4) return K::template launch<RowCfg<1, 4, 32>>(a, n_win, s);
+  if (nq <= 8) return K::template launch<RowCfg<1, 8, 32>>(a, n_win, s);
+  if (nq <= 16) return K::template launch<RowCfg<1, 16, 32>>(a, n_win, s);
+  return K::template launch<RowCfg<1, 32, 32>>(a, n_win, s);
 }
 
 // Rows per window.  Batches of up to 32768 logits in few sequences: one window, which needs no
