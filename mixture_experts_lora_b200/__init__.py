@@ -459,8 +459,11 @@ class AdamW:
             if p.dtype not in ok or g.dtype not in ok or p.shape != g.shape or p.device != dev or g.device != dev:
                 raise ValueError(f"parameter {i}: bf16 or fp32 with a gradient of its shape on {dev} is needed")
             view = _joint_view(p, g)
-            if any(n > 1 and sp == 0 for n, sp, _ in view):
-                raise ValueError(f"parameter {i} has several elements in one place")
+            reach = 1             # elements of the dimensions of smaller strides lie below this one's
+            for n, sp, _ in sorted((v for v in view if v[0] > 1), key=lambda v: v[1]):
+                if sp < reach:
+                    raise ValueError(f"parameter {i} has several elements in one place")
+                reach = sp * (n - 1) + reach
             if p.numel() and p.data_ptr() in taken:
                 raise ValueError(f"parameter {i} begins where another one does")
             taken.add(p.data_ptr())

@@ -193,7 +193,12 @@ __global__ void __launch_bounds__(kThreads, C::N <= 8 ? 4 : 2) balance_partial_k
     if (a.loss == nullptr && r0 >= t1) break;
     r0 = r0 > t0 ? r0 : t0;
     r1 = r1 < t1 ? r1 : t1;
-    if (a.loss == nullptr && r0 >= r1) continue;
+    if (a.loss == nullptr && r0 >= r1) {
+      // on to the first sequence that ends past this row, over any number of empty ones
+      const int to = block_count_le(a.S, r0, [&](int i) { return a.off[i + 1]; });
+      s = to - 1 > s ? to - 1 : s;
+      continue;
+    }
     for (int e = threadIdx.x; e < E; e += kThreads) s_cnt[e] = 0;
     if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
@@ -221,12 +226,19 @@ __global__ void __launch_bounds__(kThreads, C::N <= 8 ? 4 : 2) balance_partial_k
       px += (int64_t)step * E;
     };
     fetch();
-    // pairs per expert
-    for (int64_t i = r0 * a.k + threadIdx.x; i < r1 * a.k; i += kThreads) {
-      if (a.mask != nullptr && a.mask[(uint32_t)i / (uint32_t)a.k] == 0) continue;
-      const int e = a.ids[i];
-      if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
-      else report_error(a.err, MOE_ERR_DEVICE_INDEX);
+    // pairs per expert, four ids on their way at a time
+    for (int64_t i = r0 * a.k + threadIdx.x; i < r1 * a.k; i += 4 * kThreads) {
+      int id[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t iq = i + q * kThreads;
+        const bool in = iq < r1 * a.k && (a.mask == nullptr || a.mask[(uint32_t)iq / (uint32_t)a.k] != 0);
+        id[q] = in ? a.ids[iq] : -1;
+        if (in && (uint32_t)id[q] >= (uint32_t)E) report_error(a.err, MOE_ERR_DEVICE_INDEX);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if ((uint32_t)id[q] < (uint32_t)E) atomicAdd(&s_cnt[id[q]], 1);
     }
     for (int tw = warp * per; tw < rows; tw += step) {
       float v[C::U][C::N];
@@ -412,7 +424,16 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
       const int tu = t + u * ln.groups;
       live[u] = tu < rows && (pmask == nullptr || pmask[tu] != 0);
       if (tu < rows && tu >= s_hi) {           // on to the row's sequence
-        while (s < a.S && a.off[s + 1] <= t0 + tu) ++s;
+        if (s < a.S && a.off[s + 1] <= t0 + tu) ++s;
+        if (s < a.S && a.off[s + 1] <= t0 + tu) {        // (past empty sequences, by halves)
+          int lo = s + 1, hi = a.S;
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (a.off[mid + 1] <= t0 + tu) lo = mid + 1;
+            else hi = mid;
+          }
+          s = lo;
+        }
         s_lo = s < a.S ? (int)(a.off[s] - t0) : rows;
         s_hi = s < a.S ? (int)(a.off[s + 1] - t0) : rows;
       }
@@ -513,12 +534,12 @@ cudaError_t launch_rows(BalanceArgs& a, int64_t n_win, cudaStream_t s) {
   return K::template launch<RowCfg<1, 32, 32>>(a, n_win, s);
 }
 
-// Rows per window.  Batches of up to 32768 logits in few sequences: one window, which needs no
-// second launch.  Otherwise about four windows per SM, two above 256 experts (a block writes, and
+// Rows per window.  Batches of up to 1024 rows and 32768 logits in few sequences: one window,
+// which needs no second launch.  Otherwise about four windows per SM, two above 256 experts (a block writes, and
 // the second launch reads, a partial row per window), and 32 rows at least, less where sequences
 // are shorter (a window works through its sequences one after the other).
 int window_rows(int64_t T, int E, int S) {
-  if (T * E <= 32768 && S <= 4) return T > 0 ? (int)T : 1;
+  if (T * E <= 32768 && T <= 1024 && S <= 4) return T > 0 ? (int)T : 1;
   int64_t low = T / S;
   low = low > 32 ? 32 : low < 8 ? 8 : low;
   const int64_t windows = E <= 256 ? 592 : 296;

@@ -326,7 +326,8 @@ def test_state_dict(bits, master):
 def test_refusals():
     p = torch.zeros(8, 8, device="cuda", dtype=BF)
     for params, grads in (([p], [p[:4]]), ([p.half()], [p]), ([p], [p.double()]), ([p, p], [p, p]),
-                          ([p[:1].expand(8, 8)], [p]), ([p], [p.cpu()]), ([p], [])):
+                          ([p[:1].expand(8, 8)], [p]), ([p], [p.cpu()]), ([p], []),
+                          ([p.view(-1).as_strided((8, 8), (4, 1))], [p]), ([p.view(-1).unfold(0, 16, 8)], [torch.zeros(7, 16).to(p)])):
         with pytest.raises(ValueError):
             ml.AdamW(params, grads)
     with pytest.raises(ml.MoEError):

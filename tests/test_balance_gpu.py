@@ -113,6 +113,16 @@ def test_many_sequences_over_many_windows():
     c.check(c.run())
 
 
+@pytest.mark.parametrize("T,S,E", [(50, 200000, 16), (900, 5000, 40), (1024, 4, 32), (1025, 4, 32), (2049, 3, 8)])
+def test_many_empty_sequences(T, S, E):
+    """Runs of empty sequences inside a window; batches at the border of one window."""
+    g = np.random.default_rng(S)
+    # ends at a few places only: long runs of sequences that begin and end at one row
+    cut = np.sort(g.choice(g.integers(0, T + 1, size=7), size=S - 1)).tolist()
+    c = Case(T, E, 3, off=[0] + cut + [T], seed=T)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("E", [8, 48, 300])
 def test_masked_rows_are_not_looked_at(E):
     T, off = 90, [0, 30, 60, 80]
