@@ -411,6 +411,8 @@ STATE_BLOCK = 256     # elements that share a scale in 8-bit states
 
 def _joint_view(p, g):
     """Sizes and the two tensors' strides of a common view of at most three dimensions."""
+    if p.is_contiguous() and g.is_contiguous():
+        return [(1, 0, 0), (1, 0, 0), (p.numel(), 1, 1)]
     dims = [(n, sp, sg) for n, sp, sg in zip(p.shape, p.stride(), g.stride()) if n != 1]
     out = []
     for n, sp, sg in dims:
@@ -459,11 +461,12 @@ class AdamW:
             if p.dtype not in ok or g.dtype not in ok or p.shape != g.shape or p.device != dev or g.device != dev:
                 raise ValueError(f"parameter {i}: bf16 or fp32 with a gradient of its shape on {dev} is needed")
             view = _joint_view(p, g)
-            reach = 1             # elements of the dimensions of smaller strides lie below this one's
-            for n, sp, _ in sorted((v for v in view if v[0] > 1), key=lambda v: v[1]):
-                if sp < reach:
-                    raise ValueError(f"parameter {i} has several elements in one place")
-                reach = sp * (n - 1) + reach
+            if not p.is_contiguous():
+                reach = 1         # elements of the dimensions of smaller strides lie below this one's
+                for n, sp, _ in sorted((v for v in view if v[0] > 1), key=lambda v: v[1]):
+                    if sp < reach:
+                        raise ValueError(f"parameter {i} has several elements in one place")
+                    reach = sp * (n - 1) + reach
             if p.numel() and p.data_ptr() in taken:
                 raise ValueError(f"parameter {i} begins where another one does")
             taken.add(p.data_ptr())
