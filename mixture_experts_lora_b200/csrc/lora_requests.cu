@@ -729,21 +729,21 @@ cudaError_t launch_tiles(const LoraArgs& a, int CL, cudaStream_t s) {
 // CTAs per cluster, 1, 2 or 4: what finishes the tiles soonest if a tile takes 1 / CL and the
 // clusters that run at once are as many as measured: two CTAs per SM up to rank 32, one above, and
 // for clusters of four 33 times four CTAs on 148 SMs (clusters of 8, 15 times eight, always lost).
-// Where one CTA runs per SM a last wave of a few clusters costs as much as a full one (rank 64,
-// 35 tiles at 7168 x 4096: 58 us with 2, 65 us with 4, 101 us with 1); two per SM fill it up (rank
-// 16, 67 tiles at 2048 x 2048: 27.9 us with 4, 30.1 us with 2, 42.6 us with 1).
+// A last wave of a few clusters costs as much as a full one (rank 64, 35 tiles at 7168 x 4096:
+// 58 us with 2, 65 us with 4; rank 16, 112 tiles at 2048 x 2048: 30 us with 2, 40 us with 4), unless
+// two CTAs share an SM and it holds less than a seventh (rank 16, 67 tiles: 27.9 us with 4, 30.1 us
+// with 2, 42.6 us with 1).
 int cluster_size(int64_t T, int S, int K, int r) {
-  const double windows = (double)((T + 127) / 128);
-  const double tiles = windows + (S - 1 < windows / 2 ? S - 1 : windows / 2);   // requests cut windows
+  const double tiles = (double)((T + 127) / 128) + (S - 1);      // (requests cut windows)
   const int per_sm = r <= 32 ? 2 : 1;
   int best = 1;
   double most = 0.;
   for (int cl = 1; cl <= 4 && cl <= (K + 63) / 64; cl *= 2) {
     const double room = device_sms() * (cl < 4 ? 1. / cl : 2. / 9.) * per_sm;
-    double waves = tiles / room;
-    waves = waves < 1. ? 1. : per_sm == 1 ? std::ceil(waves) : waves;
-    if (cl / waves > most * 1.1) {           // (a cluster has its own cost)
-      most = cl / waves;
+    const double waves = std::ceil(tiles / room - (per_sm == 2 ? 0.15 : 0.));
+    const double gain = cl / (waves < 1. ? 1. : waves);
+    if (gain > most * 1.1) {               // (a cluster has its own cost)
+      most = gain;
       best = cl;
     }
   }
@@ -798,10 +798,11 @@ extern "C" moe_status_t moe_lora_requests(const moe_bf16_t* X, int64_t ldx, cons
   a.err = moe_status_word();
   if (a.err == nullptr) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Short requests row by row where there can be many of them: the launch costs a batch without
-  // any 5 us, a tile takes 16 us however few its rows, and tiles find room for a few more.
+  // Short requests in a launch of their own where there are little else (128 requests of 128 rows
+  // in all: 21 us, 25-30 us as tiles); beside prompts they find room among the tiles (4133 rows,
+  // 35 of 40 requests of one row: 27 us, 35 us with the launch).
   cudaError_t e = cudaSuccess;
-  if (seq_offsets == nullptr || (S >= 8 && T <= (int64_t)256 * S) || T <= kShortRows) {
+  if (seq_offsets == nullptr || (S >= 8 && T <= (int64_t)kShortRows * S) || T <= kShortRows) {
     ProfScope ps(K_LORA_REQUESTS, s);
     const int64_t rows = seq_offsets == nullptr ? S : (int64_t)S * kShortRows;
     const int cl = single_cluster(S);
