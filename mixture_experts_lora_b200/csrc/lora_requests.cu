@@ -103,33 +103,37 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
 }
 
 // ---------------------------------------------------------------- one row
-// One row x by a cluster.  CTA j sums x A over its share of K in fp32: A is read as it lies,
-// 16 bytes (eight ranks of one K row) a thread, GP = 2^k >= r / 8 threads side by side on a K
-// row, so that lanes GP apart hold the same ranks and a warp is summed by shuffles, the warps
-// and then the CTAs (through distributed shared memory) in a fixed order.  Then each CTA adds
-// its share of the columns: a thread takes eight columns of some rows of B.
-// A row is a chain of waits for memory, each of 1 us and under load of 3: everything whose
-// address is known goes out together (A, x, the scale and the first two rounds of B once the
-// adapter's id is there, Y before the CTAs meet), and A and B run two buffers ahead.
-constexpr int kAhead = 4;             // 16-byte pieces of A (and of B) in one of two buffers
-constexpr int kXChunk = 2048;         // values of x staged at a time
+// One row x by a cluster.  CTA j sums x A over its share of K in fp32, then adds its share of
+// the columns.  Both operands stream through one ring of shared-memory slots by bulk copies that
+// one warp issues, so that the memory is busy from the first cycle on and B arrives while the
+// CTAs exchange their sums (registers as buffers held too few bytes: 64 rows at 7168 x 2048, rank
+// 32 took OOO us, NNN us here):
+//   * a slot of A is 16 KB of the adapter's share of K rows as they lie, and those rows' x.  A
+//     thread takes 16 bytes (eight ranks of one K row), GP = 2^k >= r / 8 threads side by side
+//     on a K row, so that lanes GP apart hold the same ranks: a warp is summed by shuffles, the
+//     warps and then the CTAs (through distributed shared memory) in a fixed order;
+//   * a slot of B is some of its rows, cut to the CTA's columns.  A thread takes eight columns
+//     of every parts-th row, the parts are summed in order.
+constexpr int kConsumers = 256;             // and one warp that issues the copies
+constexpr int kSingleThreads = kConsumers + 32;
+constexpr int kSlotBytes = 16384, kSlotX = 2048, kSlots = 5;
 constexpr int kMaxCluster = 8;
 
-template <int NT>
 struct RowSmem {
-  float x[kXChunk];
-  float warp[NT / 32][128];
-  float part[kMaxCluster][128];       // every CTA's sum over its share of K
+  uint8_t slot[kSlots][kSlotBytes + kSlotX];
+  float4 out[2][kConsumers];                // partial sums of eight columns
+  float warp[kConsumers / 32][128];
+  float part[kMaxCluster][128];             // every CTA's sum over its share of K
   float xa[128];
-  float4 out[2][NT];                  // partial sums of eight columns
+  uint64_t full[kSlots], empty[kSlots];
 };
 
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// Bytes from global to this CTA's shared memory, counted by one of its mbarriers.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void add_scaled(float (&y)[8], uint4 w, float x) {
   float v[8];
@@ -138,80 +142,127 @@ __device__ __forceinline__ void add_scaled(float (&y)[8], uint4 w, float x) {
   for (int c = 0; c < 8; ++c) y[c] += x * v[c];
 }
 
-template <int NT>
-__device__ __forceinline__ void single_row(const LoraArgs& a, int64_t row, int ad, int rank, int CL,
-                                           RowSmem<NT>& sm) {
+// Requests of one row (a cluster each), or of up to kShortRows rows (a cluster per row).
+__global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraArgs a) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  RowSmem& sm = *reinterpret_cast<RowSmem*>(smem_raw);
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
-  const float scale = a.scale[ad];
-  // ---- this CTA's share of K: thread (kl, g) reads ranks 8 g .. of K rows kl, kl + lanes, ...
-  int gp = 1;
-  while (gp < a.r / 8) gp *= 2;
+  const int rank = (int)cluster_ctarank(), CL = (int)cluster_nctarank();
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&sm.full[i]), 1);
+      mbar_init(smem_u32(&sm.empty[i]), kConsumers / 32);
+    }
+    mbar_fence_init();
+  }
+  pdl_begin();
+  const int unit = (int)blockIdx.x / CL, s = a.off == nullptr ? unit : unit / kShortRows;
+  const int ad = a.adapters[s];
+  int64_t row = unit;
+  if (a.off != nullptr) {
+    const int64_t lo = a.off[s], hi = a.off[s + 1];
+    check_offsets(a.off, a.S, a.T, a.err);
+    row = lo + unit % kShortRows;
+    if (lo < 0 || hi > a.T || row >= hi || hi - lo > kShortRows) return;
+  }
+  if (ad < 0) return;                          // (the same for the cluster)
+  if (ad >= a.n_adapters) {
+    if (tid == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
+    return;
+  }
+  const int r = a.r;
+  // ---- this CTA's share of K (a multiple of 8 rows), in chunks of whole groups of 8 rows
   const int kc = ((a.K + CL - 1) / CL + 7) / 8 * 8;
   const int k0 = rank * kc < a.K ? rank * kc : a.K, k1 = k0 + kc < a.K ? k0 + kc : a.K;
-  const int g = tid & (gp - 1), kl = tid / gp, lanes = NT / gp;
-  const bool has = g * 8 < a.r;
-  const __nv_bfloat16* A = a.A + ((int64_t)ad * a.K + k0 + kl) * a.r + g * 8;
-  const int64_t a_step = (int64_t)lanes * a.r;
-  const int np = (k1 - k0 + lanes - 1) / lanes;                       // pieces (of any thread)
-  const int px = (kXChunk / lanes) & ~(kAhead - 1);                   // pieces per chunk of x
-  uint4 av[2][kAhead];
-  const auto load_a = [&](int p, uint4 (&v)[kAhead]) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      v[i] = has && k0 + kl + (p + i) * lanes < k1 ? ld_stream(A + (p + i) * a_step) : make_uint4(0u, 0u, 0u, 0u);
-  };
-  // ---- this CTA's columns: eight a thread, cp threads side by side, the rows of B over the
-  // others; passes of cp column groups, each in rounds of kAhead rows
+  const int rows_c = kSlotBytes / (r * 2) / 8 * 8;                    // (r = 8: 1024 rows, 2 KB of x)
+  const int na = (k1 - k0 + rows_c - 1) / rows_c;
+  // ---- this CTA's groups of eight columns, in passes of cp, each in chunks of rb rows of B
   const int ng = a.N / 8, ng_c = (ng + CL - 1) / CL;
-  const int g0 = rank * ng_c, g1 = g0 + ng_c < ng ? g0 + ng_c : ng;
+  const int g0 = rank * ng_c < ng ? rank * ng_c : ng, g1 = g0 + ng_c < ng ? g0 + ng_c : ng;
   int cp = 32;
-  while (cp * 2 <= (NT & -NT) && cp < ng_c) cp *= 2;
-  const int col = tid & (cp - 1), part = tid / cp, parts = NT / cp;
-  const int rounds = (a.r + parts * kAhead - 1) / (parts * kAhead);
-  const int passes = g1 > g0 ? (g1 - g0 + cp - 1) / cp : 0;
-  const __nv_bfloat16* B = a.B + (int64_t)ad * a.r * a.N;
-  uint4 bv[2][kAhead];
-  const auto load_b = [&](int pass, int round, uint4 (&v)[kAhead]) {
-    const int gi = g0 + pass * cp + col;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = (round * kAhead + i) * parts + part;
-      v[i] = pass < passes && gi < g1 && j < a.r ? ld_stream(B + (int64_t)j * a.N + (int64_t)gi * 8)
-                                                : make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
-  load_a(0, av[0]);
-  load_a(kAhead, av[1]);
-  load_b(0, 0, bv[0]);
-  load_b(rounds > 1 ? 0 : 1, rounds > 1 ? 1 : 0, bv[1]);
+  while (cp < kConsumers && cp < ng_c) cp *= 2;
+  const int passes = (g1 - g0 + cp - 1) / cp;
+  const int rb = kSlotBytes / (cp * 16) < r ? kSlotBytes / (cp * 16) : r;
+  const int nb = (r + rb - 1) / rb;
+  __syncthreads();
+  bool ok = true;
 
+  if (warp == kConsumers / 32) {
+    // ------------------------------------------------------------ copies
+    // (a launch without clusters has no cluster barrier to arrive on early: its wait would wait for
+    // this warp's own, behind copies that wait for the consumers)
+    if (CL > 1) cluster_arrive();
+    const __nv_bfloat16* A = a.A + ((int64_t)ad * a.K + k0) * r;
+    const __nv_bfloat16* X = a.X + row * a.ldx + k0;
+    const __nv_bfloat16* B = a.B + (int64_t)ad * r * a.N + (int64_t)g0 * 8;
+    const int total = na + passes * nb;
+    int it = 0;
+    for (; it < total; ++it) {
+      const int st = it % kSlots;
+      if (it >= kSlots) ok = mbar_wait(smem_u32(&sm.empty[st]), (it / kSlots - 1) & 1, a.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t bar = smem_u32(&sm.full[st]), dst = smem_u32(sm.slot[st]);
+      if (it < na) {
+        const int o = it * rows_c, n = k1 - k0 - o < rows_c ? k1 - k0 - o : rows_c;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, (uint32_t)n * (r * 2 + 2));
+          bulk_load(dst, A + (int64_t)o * r, (uint32_t)n * r * 2, bar);
+          bulk_load(dst + kSlotBytes, X + o, (uint32_t)n * 2, bar);
+        }
+      } else {
+        const int p = (it - na) / nb, j0 = (it - na) % nb * rb;
+        const int seg = g1 - g0 - p * cp < cp ? g1 - g0 - p * cp : cp;
+        const int n = r - j0 < rb ? r - j0 : rb;
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * seg) * 16);
+        __syncwarp();
+        for (int j = lane; j < n; j += 32)
+          bulk_load(dst + j * cp * 16, B + (int64_t)(j0 + j) * a.N + (int64_t)p * cp * 8, (uint32_t)seg * 16, bar);
+      }
+      __syncwarp();
+    }
+    // after a failed wait, the copies on their way land before the CTA ends
+    for (int j = it < kSlots ? 0 : it - kSlots; !ok && j < it; ++j)
+      mbar_wait(smem_u32(&sm.full[j % kSlots]), (j / kSlots) & 1, a.err);
+    __syncwarp();
+    if (CL > 1) cluster_wait();
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const float scale = a.scale[ad];
+  const auto meet = [&]() {                    // (whole warps: what came before may have split them)
+    __syncwarp();
+    named_bar(1, kConsumers);
+  };
+  int it = 0;
+  const auto wait_full = [&]() {
+    if (ok) ok = mbar_wait(smem_u32(&sm.full[it % kSlots]), (it / kSlots) & 1, a.err);
+  };
+  const auto release = [&]() {                 // (the slot's reads of this warp are done)
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.empty[it % kSlots]));
+    __syncwarp();
+    ++it;
+  };
+  int gp = 1;
+  while (gp < r / 8) gp *= 2;
+  const int g = tid & (gp - 1), kl = tid / gp, lanes = kConsumers / gp;
+  const bool has = g * 8 < r;
   float acc[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) acc[c] = 0.f;
-  const __nv_bfloat16* X = a.X + row * a.ldx + k0;
-  for (int p0 = 0; p0 < np; p0 += px) {
-    // x of px pieces (k0, the chunk and K are multiples of 8)
-    const int nx = k1 - k0 - p0 * lanes < px * lanes ? k1 - k0 - p0 * lanes : px * lanes;
-    __syncthreads();
-    for (int i = tid * 8; i < nx; i += NT * 8) {
-      float v[8];
-      unpack8(*reinterpret_cast<const uint4*>(X + p0 * lanes + i), v);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) sm.x[i + c] = v[c];
+  for (int c = 0; c < na; ++c) {
+    const int o = c * rows_c, n = k1 - k0 - o < rows_c ? k1 - k0 - o : rows_c;
+    wait_full();
+    const uint8_t* p = sm.slot[it % kSlots];
+    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(p + kSlotBytes);
+    if (has) {
+#pragma unroll 4
+      for (int k = kl; k < n; k += lanes)
+        add_scaled(acc, *reinterpret_cast<const uint4*>(p + (k * r + g * 8) * 2), __bfloat162float(x[k]));
     }
-    __syncthreads();
-    const int pe = np - p0 < px ? np - p0 : px;
-    for (int p = 0; p < pe; p += 2 * kAhead) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int o = (p + h * kAhead + i) * lanes + kl;
-          add_scaled(acc, av[h][i], o < nx ? sm.x[o] : 0.f);
-        }
-        load_a(p0 + p + (2 + h) * kAhead, av[h]);
-      }
-    }
+    release();
   }
   for (int o = gp; o < 32; o <<= 1) {
 #pragma unroll
@@ -221,55 +272,51 @@ __device__ __forceinline__ void single_row(const LoraArgs& a, int64_t row, int a
 #pragma unroll
     for (int c = 0; c < 8; ++c) sm.warp[warp][g * 8 + c] = acc[c];
   }
-  __syncthreads();
-  if (tid < a.r) {
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) v += sm.warp[i][tid];
-    const uint32_t mine = smem_u32(&sm.part[rank][tid]);
-    for (int q = 0; q < CL; ++q) st_cluster_f32(mapa_smem(mine, (uint32_t)q), v);
-  }
   // the eight elements of Y that this thread finishes in a pass
   uint4* yp = reinterpret_cast<uint4*>(a.Y + row * a.ldy) + g0 + tid;
   const auto ends = [&](int pass) { return tid < cp && g0 + pass * cp + tid < g1; };
   uint4 yv = make_uint4(0u, 0u, 0u, 0u);
   if (ends(0)) yv = *yp;
-  cluster_sync();
-  if (tid < a.r) {
+  meet();
+  if (tid < r) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kConsumers / 32; ++i) v += sm.warp[i][tid];
+    const uint32_t mine = smem_u32(&sm.part[rank][tid]);
+    for (int q = 0; q < CL; ++q) st_cluster_f32(mapa_smem(mine, (uint32_t)q), v);
+  }
+  __syncwarp();
+  if (CL > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (tid < r) {                               // (without a cluster, each thread's own value)
     float v = 0.f;
     for (int i = 0; i < CL; ++i) v += sm.part[i][tid];
     sm.xa[tid] = v * scale;
   }
-  __syncthreads();
-  int next_pass = 0, next_round = 0;      // two rounds ahead
-  const auto advance = [&]() {
-    if (++next_round == rounds) { next_round = 0; ++next_pass; }
-  };
-  advance();
-  advance();
-  int h = 0;
+  meet();
+  const int col = tid & (cp - 1), part = tid / cp, parts = kConsumers / cp;
   for (int pass = 0; pass < passes; ++pass) {
     float y[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) y[c] = 0.f;
-    for (int round = 0; round < rounds; ++round, h ^= 1) {
-      uint4 v[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) v[i] = h ? bv[1][i] : bv[0][i];
-      if (h) load_b(next_pass, next_round, bv[1]);
-      else load_b(next_pass, next_round, bv[0]);
-      advance();
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int j = (round * kAhead + i) * parts + part;
-        add_scaled(y, v[i], j < a.r ? sm.xa[j] : 0.f);
+    const bool in = g0 + pass * cp + col < g1;
+    for (int c = 0; c < nb; ++c) {
+      const int j0 = c * rb, n = r - j0 < rb ? r - j0 : rb;
+      wait_full();
+      const uint8_t* p = sm.slot[it % kSlots] + col * 16;
+      if (in) {
+#pragma unroll 4
+        for (int j = part; j < n; j += parts)
+          add_scaled(y, *reinterpret_cast<const uint4*>(p + j * cp * 16), sm.xa[j0 + j]);
       }
+      release();
     }
     // the parts of a column group, summed in order
-    if (pass > 0) __syncthreads();
     sm.out[0][tid] = make_float4(y[0], y[1], y[2], y[3]);
     sm.out[1][tid] = make_float4(y[4], y[5], y[6], y[7]);
-    __syncthreads();
+    meet();
     if (ends(pass)) {
       float v[8];
 #pragma unroll
@@ -283,33 +330,18 @@ __device__ __forceinline__ void single_row(const LoraArgs& a, int64_t row, int a
       unpack8(yv, old);
 #pragma unroll
       for (int c = 0; c < 8; ++c) v[c] += old[c];
-      yp[pass * cp] = pack8(v);
+      if (ok) yp[pass * cp] = pack8(v);
       if (ends(pass + 1)) yv = yp[(pass + 1) * cp];
     }
+    if (pass + 1 < passes) meet();
   }
 }
 
-// Requests of one row (a cluster each), or of up to kShortRows rows (a cluster per row).
-constexpr int kSingleThreads = 256;
-__global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraArgs a) {
-  pdl_begin();
-  __shared__ RowSmem<kSingleThreads> sm;
-  const int rank = (int)cluster_ctarank(), CL = (int)cluster_nctarank();
-  const int slot = (int)blockIdx.x / CL, s = a.off == nullptr ? slot : slot / kShortRows;
-  const int ad = a.adapters[s];
-  int64_t row = slot;
-  if (a.off != nullptr) {
-    const int64_t lo = a.off[s], hi = a.off[s + 1];
-    check_offsets(a.off, a.S, a.T, a.err);
-    row = lo + slot % kShortRows;
-    if (lo < 0 || hi > a.T || row >= hi || hi - lo > kShortRows) return;
-  }
-  if (ad < 0) return;                          // (the same for the cluster)
-  if (ad >= a.n_adapters) {
-    if (threadIdx.x == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
-    return;
-  }
-  single_row<kSingleThreads>(a, row, ad, rank, CL, sm);
+cudaError_t launch_single(const LoraArgs& a, int64_t rows, int CL, cudaStream_t s) {
+  const cudaError_t st = ensure_smem(lora_single_kernel, (int)sizeof(RowSmem));
+  if (st != cudaSuccess) return st;
+  ProfScope ps(K_LORA_REQUESTS, s);
+  return launch_pdl(lora_single_kernel, dim3((unsigned)(rows * CL)), dim3(kSingleThreads), sizeof(RowSmem), s, CL, a);
 }
 
 // ---------------------------------------------------------------- rows of one adapter
@@ -803,10 +835,8 @@ extern "C" moe_status_t moe_lora_requests(const moe_bf16_t* X, int64_t ldx, cons
   // 35 of 40 requests of one row: 27 us, 35 us with the launch).
   cudaError_t e = cudaSuccess;
   if (seq_offsets == nullptr || (S >= 8 && T <= (int64_t)kShortRows * S) || T <= kShortRows) {
-    ProfScope ps(K_LORA_REQUESTS, s);
     const int64_t rows = seq_offsets == nullptr ? S : (int64_t)S * kShortRows;
-    const int cl = single_cluster(S);
-    e = launch_pdl(lora_single_kernel, dim3((unsigned)(rows * cl)), dim3(kSingleThreads), 0, s, cl, a);
+    e = launch_single(a, rows, single_cluster(S), s);
     a.skip = kShortRows;
   }
   if (e == cudaSuccess && seq_offsets != nullptr && T > a.skip) {

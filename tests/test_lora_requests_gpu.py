@@ -78,6 +78,13 @@ def test_many_single_tokens(T):
     Case(T, 256, 320, 16, 11, [(7 * i) % 12 - 1 for i in range(T)]).run().check()
 
 
+@pytest.mark.parametrize("T,K,N,r", [(16, 2048, 4112, 16), (80, 2064, 8208, 24), (150, 4096, 4112, 64), (320, 1024, 4112, 128),
+                                     (300, 2048, 8192, 8)])
+def test_single_tokens_over_many_buffers(T, K, N, r):
+    """Every cluster size (8, 4, 2 and 1), more chunks than buffers, several passes over the columns."""
+    Case(T, K, N, r, 5, [i % 6 - 1 for i in range(T)]).run().check()
+
+
 @pytest.mark.parametrize("lens", [[1], [2], [8], [9], [15, 1], [127], [128], [129], [1, 1, 1], [0, 0, 3], [60, 1, 0, 200, 7],
                                   [16, 16, 16, 16], [300, 1, 1, 1, 500], [1] * 40 + [100]])
 @pytest.mark.parametrize("K,N,r", [(64, 48, 8), (320, 400, 16), (144, 656, 64)])
