@@ -441,12 +441,16 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
       f1 = tid + 1 < a.S ? o1 / C::BM + tid + 1 : INT_MAX;
     }
     __syncthreads();
-    if (tid < a.S && f0 <= slot && slot < f1) {
-      found[0] = tid; found[1] = o0; found[2] = o1; found[3] = my_ad;
+    // (offsets that decrease give a slot to several requests: every CTA of the cluster takes the last)
+    if (tid < a.S && f0 <= slot && slot < f1) atomicMax(&found[0], tid);
+    __syncthreads();
+    s = found[0];
+    if (s < 0) return;
+    if (tid == s) {
+      found[1] = o0; found[2] = o1; found[3] = my_ad;
     }
     __syncthreads();
-    s = found[0]; lo = found[1]; hi = found[2]; ad = found[3];
-    if (s < 0) return;
+    lo = found[1]; hi = found[2]; ad = found[3];
   } else {
     s = block_count_le(a.S, slot, [&](int i) { return (long long)a.off[i] / C::BM + i; }) - 1;
     if (s < 0) return;

@@ -144,6 +144,12 @@ def test_bad_adapters_and_offsets_are_reported():
         with pytest.raises(AssertionError):
             c.run()
         assert ml.moe_get_device_error() == ml.MOE_OK
+    # offsets that decrease by more than a window, so that requests claim the same rows
+    for off in ([0, 300, 100, 400], [0, 390, 10, 20, 380, 400], [0] + [400, 0] * 40 + [400]):
+        c = Case(400, 1024, 64, 8, 3, [i % 3 for i in range(len(off) - 1)], off)
+        with pytest.raises(AssertionError):
+            c.run()
+        assert ml.moe_get_device_error() == ml.MOE_OK
     c = Case(40, 64, 64, 8, 3, [0, 3], [0, 10, 40])
     before = c.Y.clone()
     c.call()
