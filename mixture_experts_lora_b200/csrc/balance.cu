@@ -314,6 +314,8 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceA
   __shared__ int s_n;
   const int warps = (int)blockDim.x / 32, warp = warp_id(), lane = lane_id(), E = a.E;
   const int rank = (int)cluster_ctarank(), ranks = a.sum_ranks, s = (int)blockIdx.x / ranks;
+  // (block 0's shared memory may be written once it runs)
+  if (ranks > 1) cluster_arrive();
   const int64_t n_win = (a.T + a.rows - 1) / a.rows;
   const int64_t r0 = a.off != nullptr ? a.off[s] : 0, r1 = a.off != nullptr ? a.off[s + 1] : a.T;
   // first and last window of the sequence (none if it is empty), within the table whatever
@@ -374,10 +376,13 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceA
   }
   const float mine = block_sum(part, s_part);
   if (ranks > 1) {
+    __syncwarp();
+    cluster_wait();
     if (threadIdx.x == 0) {
       const uint32_t dst = mapa_smem(smem_u32(&s_loss[rank]), 0u);
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(mine) : "memory");
     }
+    __syncwarp();
     cluster_sync();
   }
   if (rank == 0 && threadIdx.x == 0) {

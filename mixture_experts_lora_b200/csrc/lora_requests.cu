@@ -5,7 +5,7 @@
 // prompts, by latency for a few tokens.  Two forms:
 //
 // lora_tiles_kernel, for requests of any length.  Rows are cut into windows of 128; a
-// cluster of 1 to 8 CTAs owns the rows of one request within one window and runs both
+// cluster of 1 to 4 CTAs owns the rows of one request within one window and runs both
 // products in one launch, so that X A never leaves the chip:
 //   1. X A: each CTA sums its share of K, 64 columns a stage: TMA brings the rows of X and
 //      64 rows of A, tcgen05.mma adds S[128 x RP] in TMEM;
@@ -59,12 +59,6 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ void st_cluster_u4(uint32_t addr, uint4 v) {
   asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
@@ -107,7 +101,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
 // the columns.  Both operands stream through one ring of shared-memory slots by bulk copies that
 // one warp issues, so that the memory is busy from the first cycle on and B arrives while the
 // CTAs exchange their sums (registers as buffers held too few bytes: 64 rows at 7168 x 2048, rank
-// 32 took OOO us, NNN us here):
+// 32 took 13.6 us a call, 12.3 us here):
 //   * a slot of A is 16 KB of the adapter's share of K rows as they lie, and those rows' x.  A
 //     thread takes 16 bytes (eight ranks of one K row), GP = 2^k >= r / 8 threads side by side
 //     on a K row, so that lanes GP apart hold the same ranks: a warp is summed by shuffles, the
@@ -186,12 +180,20 @@ __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraA
   const int nb = (r + rb - 1) / rb;
   __syncthreads();
   bool ok = true;
+  // Two cluster barriers: every CTA runs, so that its shared memory may be written; every CTA's
+  // sums are written.  (Only in a cluster: without one a barrier would make the consumers wait
+  // for the copy warp, which waits for them.)
+  if (CL > 1) cluster_arrive();
 
   if (warp == kConsumers / 32) {
     // ------------------------------------------------------------ copies
-    // (a launch without clusters has no cluster barrier to arrive on early: its wait would wait for
-    // this warp's own, behind copies that wait for the consumers)
-    if (CL > 1) cluster_arrive();
+    bool met = CL == 1;
+    const auto go_on = [&]() {                 // (once the first copies are on their way)
+      if (met) return;
+      cluster_wait();
+      cluster_arrive();
+      met = true;
+    };
     const __nv_bfloat16* A = a.A + ((int64_t)ad * a.K + k0) * r;
     const __nv_bfloat16* X = a.X + row * a.ldx + k0;
     const __nv_bfloat16* B = a.B + (int64_t)ad * r * a.N + (int64_t)g0 * 8;
@@ -199,6 +201,7 @@ __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraA
     int it = 0;
     for (; it < total; ++it) {
       const int st = it % kSlots;
+      if (it == kSlots) go_on();
       if (it >= kSlots) ok = mbar_wait(smem_u32(&sm.empty[st]), (it / kSlots - 1) & 1, a.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -221,6 +224,7 @@ __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraA
       }
       __syncwarp();
     }
+    go_on();
     // after a failed wait, the copies on their way land before the CTA ends
     for (int j = it < kSlots ? 0 : it - kSlots; !ok && j < it; ++j)
       mbar_wait(smem_u32(&sm.full[j % kSlots]), (j / kSlots) & 1, a.err);
@@ -278,6 +282,7 @@ __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraA
   uint4 yv = make_uint4(0u, 0u, 0u, 0u);
   if (ends(0)) yv = *yp;
   meet();
+  if (CL > 1) cluster_wait();
   if (tid < r) {
     float v = 0.f;
 #pragma unroll
@@ -786,6 +791,16 @@ int cluster_size(int64_t T, int S, int K, int r) {
   return best;
 }
 
+// Whether an element of the T rows of K from x on, ldx apart, is one of the T rows of N from y on.
+bool rows_overlap(const moe_bf16_t* x, int64_t ldx, int64_t K, const moe_bf16_t* y, int64_t ldy, int64_t N, int64_t T) {
+  const int64_t d = (reinterpret_cast<intptr_t>(y) - reinterpret_cast<intptr_t>(x)) / (int64_t)sizeof(moe_bf16_t);
+  if (d >= (T - 1) * ldx + K || -d >= (T - 1) * ldy + N) return false;
+  // interleaved rows of one buffer: their columns must lie apart
+  if (ldx != ldy) return true;
+  const int64_t c = ((d % ldx) + ldx) % ldx;      // Y's first column within X's rows
+  return c < K || c + N > ldx;
+}
+
 // CTAs per row of lora_single_kernel: 8 while all clusters find a place at once (15 of 8 CTAs),
 // then what keeps the CTAs within two per SM (64 rows at 7168 x 2048, rank 32: 14 us with 8,
 // 10.2 us with 4, 11.2 us with 2, 19 us with 1).
@@ -814,6 +829,7 @@ extern "C" moe_status_t moe_lora_requests(const moe_bf16_t* X, int64_t ldx, cons
   if (ldx < K || ldy < N || ldx % 8 != 0 || ldy % 8 != 0) return MOE_ERR_INVALID_ARG;
   if (T == 0 || S == 0) return MOE_OK;
   if (!aligned16(X) || !aligned16(Y) || adapters == nullptr) return MOE_ERR_INVALID_ARG;
+  if (rows_overlap(X, ldx, K, Y, ldy, N, T)) return MOE_ERR_INVALID_ARG;
   if (n_adapters > 0 && (!aligned16(A) || !aligned16(B) || scale == nullptr)) return MOE_ERR_INVALID_ARG;
   LoraArgs a{};
   a.X = reinterpret_cast<const __nv_bfloat16*>(X);

@@ -349,3 +349,20 @@ def test_trains_a_small_problem():
         ref.step()
     # 20 steps, each 70 u of an update below 0.1 and of weights below 8
     assert (p.double() - q.detach()).abs().max() <= 20 * 70 * U * 8
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_elements_past_32_bits(bits):
+    """A tensor of more than 2^31 elements whose last ones move as they do in a tensor of their own."""
+    n, tail = (1 << 31) + 1000, 700
+    p, g = torch.zeros(n, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator().manual_seed(4)
+    sp = torch.randn(tail, generator=gen).bfloat16().cuda()
+    sg = torch.randn(tail, generator=gen).bfloat16().cuda()
+    p[-tail:], g[-tail:] = sp, sg
+    kw = dict(lr=0.01, weight_decay=0.1, state_bits=bits)
+    ml.AdamW([p], [g], **kw).step()
+    ml.AdamW([sp], [sg], **kw).step()
+    torch.cuda.synchronize()
+    assert torch.equal(p[-tail:], sp)
+    assert not p[:-tail].any()

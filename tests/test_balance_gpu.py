@@ -254,3 +254,36 @@ def test_beside_the_router_backward(name):
     c = Case(cfg.T, cfg.E, cfg.k, ids=buf.ids.cpu().long(), logits=cpu["logits"])
     c.dloss = bal.dloss.cpu()
     c.check((bal.loss.cpu(), bal.counts.cpu(), bal.n_tokens.cpu(), bal.dlogits.cpu()), base.cpu())
+
+
+def test_logits_past_32_bits():
+    """More than 2^31 logits, the last rows a sequence of their own: the same as those rows alone.
+    A row sum runs over at most 1000 rows a warp and 50 partial sums, so 2000 u + E u bounds the rest."""
+    T, E, k, tail = (1 << 21) + 3000, 1024, 2, 40
+    dev = dict(device="cuda")
+    x, grad = torch.zeros(T, E, **dev), torch.empty(T, E, **dev)
+    ids = torch.zeros(T, k, dtype=torch.int32, **dev)
+    ids[:, 1] = 1
+    small = Case(tail, E, k, seed=3)
+    x[-tail:], ids[-tail:] = small.logits.cuda(), small.ids.cuda()
+    small.dloss = torch.ones(1)
+    want = small.run()
+    off = torch.tensor([0, T - tail, T], dtype=torch.int32, **dev)
+    loss, counts, n = torch.empty(2, **dev), torch.empty(2, E, dtype=torch.int32, **dev), torch.empty(2, dtype=torch.int32, **dev)
+    ws = torch.empty(ml.moe_balance_workspace_bytes(T, E, 2), dtype=torch.uint8, **dev)
+    ml.moe_balance_loss(x, ids, loss, counts, n, ws, off)
+    ml.moe_balance_loss_backward(x, counts, n, torch.ones(2, **dev), k, grad, off)
+    assert ml.moe_get_device_error() == ml.MOE_OK
+    assert torch.equal(counts[1:].cpu(), want[1]) and n.tolist() == [T - tail, tail]
+    assert counts[0, :2].tolist() == [T - tail] * 2 and not counts[0, 2:].any()
+    tol = (2000 + E) * U
+    assert abs(loss[1].item() - want[0].item()) <= 2 * tol * want[0].item() and abs(loss[0].item() - 1) <= tol
+    small.check((want[0], want[1], want[2], grad[-tail:].cpu()))
+    # uniform rows: E / (k n^2) (count - n k / E) / E, the counts n, n, 0, 0, ...
+    N = T - tail
+    for row in (0, N // 2, N - 1):
+        r = grad[row].double().cpu()
+        f = torch.zeros(E, dtype=torch.float64)
+        f[:2] = N
+        ref = (f - f.sum() / E) / (k * N * N)
+        assert (r - ref).abs().max() <= (3 * E + 64) * U * 2 / (k * N)

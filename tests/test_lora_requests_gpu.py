@@ -115,9 +115,59 @@ def test_strided_rows(single, ldx, ldy):
     Case(T, 160, 144, 16, 2, ad, off, ldx=ldx, ldy=ldy).run().check()
 
 
+@pytest.mark.parametrize("off", [None, [0, 5, 150]])
+@pytest.mark.parametrize("first", ["X", "Y"])
+def test_rows_side_by_side_in_one_buffer(off, first):
+    """X and Y as columns of one buffer, with columns between and behind them that stay."""
+    T, K, N = (20 if off is None else 150), 96, 80
+    ad = [i % 2 for i in range(T if off is None else 2)]
+    c = Case(T, K, N, 16, 2, ad, off)
+    buf = torch.randn(T, K + N + 24).to(BF).cuda()
+    x0, y0 = (0, K + 16) if first == "X" else (N + 16, 0)
+    c.X, c.Y = buf[:, x0:x0 + K], buf[:, y0:y0 + N]
+    c.Ys, c.ldy = c.Y, 0
+    start = buf.clone()
+    c.run().check()
+    rest = torch.ones(buf.shape[1], dtype=torch.bool)
+    rest[y0:y0 + N] = False
+    assert torch.equal(buf[:, rest.cuda()], start[:, rest.cuda()])
+
+
 def test_long_and_wide():
     Case(3000, 2048, 1536, 16, 4, [0, 3, 1], [0, 1100, 1101, 2990]).run().check()
     Case(700, 7168, 2048, 32, 2, [1, 0], [0, 350, 700]).run().check()
+
+
+def test_many_packed_requests():
+    """More requests than a block has threads, most of them short, beside prompts."""
+    g = torch.Generator().manual_seed(5)
+    lens = torch.randint(0, 4, (400,), generator=g).tolist()
+    lens[3], lens[170], lens[399] = 700, 900, 260
+    off = np.cumsum([2] + lens).tolist()
+    Case(off[-1] + 3, 192, 144, 16, 5, [i % 6 - 1 for i in range(400)], off).run().check()
+
+
+def test_rows_past_32_bits():
+    """Rows of Y (and of X) that begin past 2^31 elements."""
+    ld, T = 4096, (1 << 19) + 300
+    Y = torch.zeros(T, ld, dtype=BF, device="cuda")
+    X = torch.zeros(T, ld, dtype=BF, device="cuda")
+    A, B = torch.ones(1, 64, 8, dtype=BF, device="cuda"), torch.ones(1, 8, 32, dtype=BF, device="cuda")
+    X[-200:, :64] = 0.5
+    scale = torch.ones(1, device="cuda")
+    idx = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")      # noqa: E731
+    for off, ad in (([0, T - 200, T], [-1, 0]), ([0, T - 3, T], [-1, 0]), (None, None)):
+        if off is None:
+            ad = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+            ad[-3:] = 0
+        else:
+            ad = idx(ad)
+        Y.zero_()
+        ml.moe_lora_requests(X[:, :64], ad, A, B, scale, Y[:, :32], None if off is None else idx(off))
+        n = 200 if off is not None and off[1] == T - 200 else 3
+        assert torch.equal(Y[-n:, :32], torch.full((n, 32), 256.0, dtype=BF, device="cuda"))
+        assert not Y[:-n].any() and not Y[-n:, 32:].any()
+    assert ml.moe_get_device_error() == ml.MOE_OK
 
 
 def test_not_finite_rows_keep_to_themselves():

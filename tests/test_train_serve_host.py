@@ -90,6 +90,17 @@ def test_lora_requests_refusals(L):
     assert call(T=0, S=0, X=None, Y=None) == ml.MOE_OK
 
 
+def test_lora_requests_refuses_rows_that_overlap(L):
+    def call(x, ldx, y, ldy, T=8, K=64, N=32):
+        return L.moe_lora_requests(P(x), ldx, None, FAKE, T, T, FAKE, FAKE, FAKE, 2, K, N, 8, P(y), ldy, None)
+    at = 1 << 20
+    for y, ldx, ldy in ((at, 64, 64), (at + 112, 64, 64), (at - 16, 64, 32), (at + 2 * (7 * 64 + 56), 64, 32),
+                        (at + 2 * 40, 96, 96), (at + 2 * 72, 96, 96), (at - 2 * 24, 96, 96), (at + 2 * (7 * 96 + 56), 96, 96),
+                        (at + 2 * 64, 96, 104), (at - 2 * 7 * 96, 96, 96)):
+        assert call(at, ldx, y, ldy) == ml.MOE_ERR_INVALID_ARG, (y - at, ldx, ldy)
+    assert call(at, 64, at + 2 * 56, 32, T=1) == call(at, 64, at - 2 * 24, 32, T=1) == ml.MOE_ERR_INVALID_ARG
+
+
 def test_bindings_refuse_cpu_tensors_and_wrong_types():
     z, i = torch.zeros, torch.int32
     with pytest.raises(ValueError):
