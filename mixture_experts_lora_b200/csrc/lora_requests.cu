@@ -802,8 +802,9 @@ bool rows_overlap(const moe_bf16_t* x, int64_t ldx, int64_t K, const moe_bf16_t*
 }
 
 // CTAs per row of lora_single_kernel: 8 while all clusters find a place at once (15 of 8 CTAs),
-// then what keeps the CTAs within two per SM (64 rows at 7168 x 2048, rank 32: 14 us with 8,
-// 10.2 us with 4, 11.2 us with 2, 19 us with 1).
+// then what keeps the CTAs within two per SM (at 7168 x 2048, rank 32, with 8, 4, 2 and 1: 15 rows
+// 6.2, 7.7, 11.2, 16.9 us; 64 rows 14.4, 10.0, 11.5, 17.0 us; 128 rows 27.7, 18.7, 14.5, 17.3 us;
+// 296 rows 63, 42, 28.2, 23.5 us).
 int single_cluster(int64_t S) {
   if (S <= 15) return 8;
   int cl = 4;
