@@ -313,7 +313,7 @@ def _launch(name, index, stream, *args):
     """Calls the library's function `name` with device `index` current and, as its last argument,
     `stream` or that device's current one."""
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         _check(name, getattr(lib(), name)(*args, raw))
     else:
         with torch.cuda.device(index):

@@ -14,7 +14,7 @@
 // group before it works on the first, so that enough bytes are on their way.
 // Forward: the lanes sum their experts' probabilities over the rows, the block's warps are
 // summed in a fixed order through shared memory, and each (window, sequence) pair writes one
-// partial row; a second launch sums a sequence's partials in window order.  A batch of one
+// partial row; a second launch sums a sequence's partials in a fixed order.  A batch of one
 // window needs no second launch.  Everything is fp32 (counts: integers).
 #include "common.cuh"
 #include "internal.h"
@@ -225,20 +225,37 @@ __global__ void __launch_bounds__(kThreads, C::N <= 8 ? 4 : 2) balance_partial_k
       t += step;
       px += (int64_t)step * E;
     };
-    fetch();
-    // pairs per expert, four ids on their way at a time
-    for (int64_t i = r0 * a.k + threadIdx.x; i < r1 * a.k; i += 4 * kThreads) {
-      int id[4];
+    // pairs per expert, eight ids on their way at a time, the first of them ahead of the logits: the
+    // counting ends while those arrive (131072 x 128, both launches: 23.7 us, 25.4 us with four
+    // ids at a time behind the logits)
+    constexpr int IDS = 8;
+    const int pairs = rows * a.k;
+    const int32_t* ids = a.ids + r0 * a.k;
+    int id[IDS];
+    uint32_t valid = 0;
+    const auto load_ids = [&](int first) {
+      valid = 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t iq = i + q * kThreads;
-        const bool in = iq < r1 * a.k && (a.mask == nullptr || a.mask[(uint32_t)iq / (uint32_t)a.k] != 0);
-        id[q] = in ? a.ids[iq] : -1;
-        if (in && (uint32_t)id[q] >= (uint32_t)E) report_error(a.err, MOE_ERR_DEVICE_INDEX);
+      for (int q = 0; q < IDS; ++q) {
+        if (first + q * kThreads >= pairs) break;                // (the same for the block)
+        const int i = first + q * kThreads + threadIdx.x;
+        const bool in = i < pairs && (pmask == nullptr || pmask[(uint32_t)i / (uint32_t)a.k] != 0);
+        valid |= (uint32_t)in << q;
+        if (in) id[q] = __ldg(ids + i);
       }
+    };
+    load_ids(0);
+    fetch();
+    for (int first = 0; first < pairs;) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < IDS; ++q) {
+        if (first + q * kThreads >= pairs) break;
+        if (((valid >> q) & 1) == 0) continue;
         if ((uint32_t)id[q] < (uint32_t)E) atomicAdd(&s_cnt[id[q]], 1);
+        else report_error(a.err, MOE_ERR_DEVICE_INDEX);
+      }
+      first += IDS * kThreads;
+      load_ids(first);
     }
     for (int tw = warp * per; tw < rows; tw += step) {
       float v[C::U][C::N];
@@ -302,20 +319,30 @@ __global__ void __launch_bounds__(kThreads, C::N <= 8 ? 4 : 2) balance_partial_k
   }
 }
 
-// A cluster per sequence: its partial rows summed in window order (a warp every warps-th window,
-// then the warps in order).  Block b of the cluster sums every cluster-th group of 32 experts;
-// block 0 adds the blocks' parts of the loss in order.
-constexpr int kSumThreads = 1024;
+// A cluster per sequence sums its partial rows.  Experts are taken in groups of 128, four a lane;
+// the cluster's CTAs share the groups and, where there are more CTAs, each group's windows.  A warp
+// sums every so-manyth window, then the CTA's warps and the CTAs are summed, all in a fixed
+// order.  Four windows of a warp are on their way at once, so that up to 1024 windows of 128 experts
+// need one wait for memory (131072 x 128, 592 windows, both launches: 19.9 us, 23.7 us where each of
+// four CTAs took all windows of 32 experts).
+constexpr int kSumThreads = 1024, kGroup = 128, kMaxRanks = 8;
+template <bool V4>
 __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceArgs a) {
   pdl_begin();
-  __shared__ float s_sum[32][33];
-  __shared__ int s_cnt[32][33];
-  __shared__ float s_part[32], s_loss[8];
+  __shared__ __align__(16) float s_sum[32][kGroup];
+  __shared__ __align__(16) int s_cnt[32][kGroup];
+  __shared__ float r_sum[kMaxRanks][kGroup];     // the other CTAs' parts
+  __shared__ int r_cnt[kMaxRanks][kGroup];
+  __shared__ float s_part[32], s_loss[kMaxRanks];
   __shared__ int s_n;
-  const int warps = (int)blockDim.x / 32, warp = warp_id(), lane = lane_id(), E = a.E;
+  const int warps = (int)blockDim.x / 32, warp = warp_id(), lane = lane_id(), tid = (int)threadIdx.x, E = a.E;
   const int rank = (int)cluster_ctarank(), ranks = a.sum_ranks, s = (int)blockIdx.x / ranks;
-  // (block 0's shared memory may be written once it runs)
   if (ranks > 1) cluster_arrive();
+  // CTA (re, wr): groups re, re + rE, ... and of their windows the wr-th part; with rW > 1 one group
+  const int groups = (E + kGroup - 1) / kGroup;
+  int rE = 1;
+  while (rE < ranks && rE < groups) rE *= 2;
+  const int rW = ranks / rE, re = rank % rE, wr = rank / rE;
   const int64_t n_win = (a.T + a.rows - 1) / a.rows;
   const int64_t r0 = a.off != nullptr ? a.off[s] : 0, r1 = a.off != nullptr ? a.off[s + 1] : a.T;
   // first and last window of the sequence (none if it is empty), within the table whatever
@@ -326,70 +353,120 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceA
     w1 = (r1 - 1) / a.rows + 1;
     if (w1 > n_win) w1 = n_win;
   }
-  if (threadIdx.x == 0) s_n = 0;
+  if (tid == 0) s_n = 0;
   __syncthreads();
-  int n = 0;
-  for (int64_t w = w0 + threadIdx.x; w < w1; w += blockDim.x) n += a.pn[w + s];
-  if (n != 0) atomicAdd(&s_n, n);
+  if (rank == 0) {
+    int n = 0;
+    for (int64_t w = w0 + tid; w < w1; w += blockDim.x) n += a.pn[w + s];
+    if (n != 0) atomicAdd(&s_n, n);
+  }
   float part = 0.f;
-  for (int e0 = rank * 32; e0 < E; e0 += ranks * 32) {
-    const int e = e0 + lane;
-    float sum = 0.f;
-    int cnt = 0;
-    if (e < E) {
-      const float* ps = a.psum + s * (int64_t)E + e;
-      const int32_t* pc = a.pcnt + s * (int64_t)E + e;
-      int64_t w = w0 + warp;
-      for (; w + 3 * warps < w1; w += 4 * warps) {       // four loads of each on their way
-        float v[4];
-        int c[4];
+  const auto finish = [&](int e, float v, int c) {
+    if (e >= E) return;
+    a.out_counts[(int64_t)s * E + e] = c;
+    part += (float)c * v;
+  };
+  bool started = ranks == 1;
+  for (int g = re; g < groups; g += rE) {
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    int cnt[4] = {0, 0, 0, 0};
+    const int e0 = g * kGroup + (V4 ? 4 * lane : lane);
+    const int64_t step = (int64_t)rW * warps;
+    for (int64_t w = w0 + wr * warps + warp; w < w1; w += 4 * step) {
+      float v[4][4];
+      int c[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = ps[(w + i * warps) * E];
-          c[i] = pc[(w + i * warps) * E];
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int64_t at = (w + i * step + s) * E + e0;
+        const bool in = w + i * step < w1;
+        if constexpr (V4) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          int4 y = make_int4(0, 0, 0, 0);
+          if (in && e0 < E) {
+            x = *reinterpret_cast<const float4*>(a.psum + at);
+            y = *reinterpret_cast<const int4*>(a.pcnt + at);
+          }
+          v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
+          c[i][0] = y.x; c[i][1] = y.y; c[i][2] = y.z; c[i][3] = y.w;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum += v[i];
-          cnt += c[i];
+          for (int j = 0; j < 4; ++j) {
+            const bool here = in && e0 + 32 * j < E;
+            v[i][j] = here ? a.psum[at + 32 * j] : 0.f;
+            c[i][j] = here ? a.pcnt[at + 32 * j] : 0;
+          }
         }
       }
-      for (; w < w1; w += warps) {
-        sum += ps[w * E];
-        cnt += pc[w * E];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sum[j] += v[i][j];
+          cnt[j] += c[i][j];
+        }
+    }
+    __syncthreads();                             // the last group's sums are read
+    if constexpr (V4) {
+      *reinterpret_cast<float4*>(&s_sum[warp][4 * lane]) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+      *reinterpret_cast<int4*>(&s_cnt[warp][4 * lane]) = make_int4(cnt[0], cnt[1], cnt[2], cnt[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s_sum[warp][lane + 32 * j] = sum[j];
+        s_cnt[warp][lane + 32 * j] = cnt[j];
       }
     }
-    __syncthreads();                                     // the last group's sums are read
-    s_sum[warp][lane] = sum;
-    s_cnt[warp][lane] = cnt;
     __syncthreads();
-    if (warp == 0 && e < E) {
+    if (!started) {                              // (long past: the CTAs of the cluster run)
+      cluster_wait();
+      started = true;
+    }
+    if (tid < kGroup) {
       float v = 0.f;
       int c = 0;
+#pragma unroll 8
       for (int i = 0; i < warps; ++i) {
-        v += s_sum[i][lane];
-        c += s_cnt[i][lane];
+        v += s_sum[i][tid];
+        c += s_cnt[i][tid];
       }
-      a.out_counts[(int64_t)s * E + e] = c;
-      part += (float)c * v;
+      if (rW == 1) {
+        finish(g * kGroup + tid, v, c);
+      } else {                                   // to the group's first CTA
+        const uint32_t dv = mapa_smem(smem_u32(&r_sum[wr][tid]), (uint32_t)re);
+        const uint32_t dc = mapa_smem(smem_u32(&r_cnt[wr][tid]), (uint32_t)re);
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dv), "f"(v) : "memory");
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dc), "r"(c) : "memory");
+      }
+    }
+  }
+  if (!started) cluster_wait();                  // (a CTA without a group)
+  if (rW > 1) {
+    __syncwarp();
+    cluster_sync();
+    if (wr == 0 && re < groups && tid < kGroup) {
+      float v = 0.f;
+      int c = 0;
+      for (int i = 0; i < rW; ++i) {
+        v += r_sum[i][tid];
+        c += r_cnt[i][tid];
+      }
+      finish(re * kGroup + tid, v, c);
     }
   }
   const float mine = block_sum(part, s_part);
-  if (ranks > 1) {
-    __syncwarp();
-    cluster_wait();
-    if (threadIdx.x == 0) {
-      const uint32_t dst = mapa_smem(smem_u32(&s_loss[rank]), 0u);
+  if (rE > 1) {
+    if (tid == 0 && wr == 0) {
+      const uint32_t dst = mapa_smem(smem_u32(&s_loss[re]), 0u);
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(mine) : "memory");
     }
     __syncwarp();
     cluster_sync();
   }
-  if (rank == 0 && threadIdx.x == 0) {
+  if (rank == 0 && tid == 0) {
     float all = mine;
-    if (ranks > 1) {
+    if (rE > 1) {
       all = 0.f;
-      for (int i = 0; i < ranks; ++i) all += s_loss[i];
+      for (int i = 0; i < rE; ++i) all += s_loss[i];
     }
     a.loss[s] = all * loss_factor(E, a.k, s_n);
     a.out_n[s] = s_n;
@@ -625,12 +702,15 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_ids, int6
   if (!one) {
     a.loss = loss;
     ProfScope ps(K_BALANCE_SUM, s);
-    // many windows per sequence: large blocks, and up to 8 of them where sequences are few
+    // many windows per sequence: large blocks; as many of them as find work, while there are SMs
     const bool many = L.n_win > 32 * (int64_t)S;
+    const int64_t parts = ((E + kGroup - 1) / kGroup) * (L.n_win / S / 32 + 1);
     a.sum_ranks = 1;
-    while (a.sum_ranks < 8 && a.sum_ranks * 32 < E && S * (int64_t)a.sum_ranks < device_sms()) a.sum_ranks *= 2;
-    if (launch_pdl(balance_sum_kernel, dim3((unsigned)S * a.sum_ranks), dim3(many ? kSumThreads : kThreads), 0, s,
-                   a.sum_ranks, a) != cudaSuccess)
+    while (a.sum_ranks < kMaxRanks && a.sum_ranks < parts && S * (int64_t)a.sum_ranks < device_sms()) a.sum_ranks *= 2;
+    const dim3 grid((unsigned)S * a.sum_ranks), block(many ? kSumThreads : kThreads);
+    const cudaError_t e = E % 4 == 0 ? launch_pdl(balance_sum_kernel<true>, grid, block, 0, s, a.sum_ranks, a)
+                                     : launch_pdl(balance_sum_kernel<false>, grid, block, 0, s, a.sum_ranks, a);
+    if (e != cudaSuccess)
       return MOE_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

@@ -256,6 +256,14 @@ def test_beside_the_router_backward(name):
     c.check((bal.loss.cpu(), bal.counts.cpu(), bal.n_tokens.cpu(), bal.dlogits.cpu()), base.cpu())
 
 
+@pytest.mark.parametrize("T,E,k,cuts", [(40000, 256, 8, ()), (40001, 130, 4, (17, 20000)), (20000, 1000, 6, (19999,)),
+                                        (30000, 384, 2, ()), (50000, 60, 4, (1, 49000)), (20000, 1023, 3, (5000, 10000)),
+                                        (60000, 33, 2, ()), (6000, 128, 8, (3000,))])
+def test_few_sequences_over_many_windows(T, E, k, cuts):
+    c = Case(T, E, k, None if not cuts else [0, *cuts, T])
+    c.check(c.run())
+
+
 def test_logits_past_32_bits():
     """More than 2^31 logits, the last rows a sequence of their own: the same as those rows alone.
     A row sum runs over at most 1000 rows a warp and 50 partial sums, so 2000 u + E u bounds the rest."""
