@@ -328,7 +328,6 @@ __global__ void __launch_bounds__(kThreads, C::N <= 8 ? 4 : 2) balance_partial_k
 constexpr int kSumThreads = 1024, kGroup = 128, kMaxRanks = 8;
 template <bool V4>
 __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceArgs a) {
-  pdl_begin();
   __shared__ __align__(16) float s_sum[32][kGroup];
   __shared__ __align__(16) int s_cnt[32][kGroup];
   __shared__ float r_sum[kMaxRanks][kGroup];     // the other CTAs' parts
@@ -337,29 +336,29 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceA
   __shared__ int s_n;
   const int warps = (int)blockDim.x / 32, warp = warp_id(), lane = lane_id(), tid = (int)threadIdx.x, E = a.E;
   const int rank = (int)cluster_ctarank(), ranks = a.sum_ranks, s = (int)blockIdx.x / ranks;
-  if (ranks > 1) cluster_arrive();
   // CTA (re, wr): groups re, re + rE, ... and of their windows the wr-th part; with rW > 1 one group
   const int groups = (E + kGroup - 1) / kGroup;
   int rE = 1;
   while (rE < ranks && rE < groups) rE *= 2;
   const int rW = ranks / rE, re = rank % rE, wr = rank / rE;
-  const int64_t n_win = (a.T + a.rows - 1) / a.rows;
+  const int n_win = (int)((uint32_t)(a.T + a.rows - 1) / (uint32_t)a.rows);     // (T < 2^31)
+  if (tid == 0) s_n = 0;
+  if (ranks > 1) cluster_arrive();
+  pdl_begin();
   const int64_t r0 = a.off != nullptr ? a.off[s] : 0, r1 = a.off != nullptr ? a.off[s + 1] : a.T;
   // first and last window of the sequence (none if it is empty), within the table whatever
   // the offsets hold
   int64_t w0 = 0, w1 = 0;
-  if (r0 >= 0 && r1 > r0) {
-    w0 = r0 / a.rows;
-    w1 = (r1 - 1) / a.rows + 1;
+  if (a.off == nullptr) {
+    w1 = n_win;
+  } else if (r0 >= 0 && r1 > r0) {
+    w0 = (uint32_t)r0 / (uint32_t)a.rows;
+    w1 = (uint32_t)(r1 - 1) / (uint32_t)a.rows + 1;
     if (w1 > n_win) w1 = n_win;
   }
-  if (tid == 0) s_n = 0;
-  __syncthreads();
-  if (rank == 0) {
-    int n = 0;
+  int n = 0;                                     // (added up below, with the sums on their way)
+  if (rank == 0)
     for (int64_t w = w0 + tid; w < w1; w += blockDim.x) n += a.pn[w + s];
-    if (n != 0) atomicAdd(&s_n, n);
-  }
   float part = 0.f;
   const auto finish = [&](int e, float v, int c) {
     if (e >= E) return;
@@ -406,6 +405,8 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceA
         }
     }
     __syncthreads();                             // the last group's sums are read
+    if (n != 0) atomicAdd(&s_n, n);
+    n = 0;
     if constexpr (V4) {
       *reinterpret_cast<float4*>(&s_sum[warp][4 * lane]) = make_float4(sum[0], sum[1], sum[2], sum[3]);
       *reinterpret_cast<int4*>(&s_cnt[warp][4 * lane]) = make_int4(cnt[0], cnt[1], cnt[2], cnt[3]);
