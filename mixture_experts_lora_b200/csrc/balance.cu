@@ -523,6 +523,14 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
       live[u] = live[u] && tu >= s_lo;
       seq[u] = s;
       load_row<C>(px + u * ln.groups * E, E, ln, live[u], v[u]);
+      // what is added to is on its way to L2 meanwhile (131072 x 128 added: 35.8 us, 40.5 us
+      // without; asking for the next rows too took 43 to 46 us)
+      if (a.accumulate && live[u]) {
+#pragma unroll
+        for (int q = 0; q < C::NQ; ++q)
+          if (expert_of<C>(ln, q) < E)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(po + u * ln.groups * E + q * ln.L * C::V));
+      }
     }
 #pragma unroll
     for (int u = 0; u < C::U; ++u) {
