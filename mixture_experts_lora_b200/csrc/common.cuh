@@ -441,6 +441,16 @@ __device__ __forceinline__ bool named_bar_or(int id, int n, bool pred) {
   return r != 0;
 }
 
+// One lane of a converged warp, chosen so that the compiler knows that it is one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ int warp_id() { return threadIdx.x >> 5; }
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 31; }
 

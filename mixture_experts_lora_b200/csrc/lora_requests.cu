@@ -363,11 +363,11 @@ struct TilesCfg {
   static constexpr int OP_BYTES = OP_ATOMS * BM * 128;
   static constexpr int PART_BYTES = BM * RP * 4;          // exchanged partial (clusters only)
   static constexpr int BAR_BYTES = 256;
-  static constexpr int TMEM_COLS = 128;                   // two 64-column accumulators; S before them
-  // two groups of four epilogue warps (the second stage by stage in turn with the first), loader,
-  // MMA issuer
-  static constexpr int THREADS = 320;
-  static constexpr int LOADER = 8, ISSUER = 9;
+  static constexpr int ND = 4, TMEM_COLS = ND * 64;       // accumulators of 64 columns; S before them
+  // two groups of four epilogue warps (the second stage by stage in turn with the first), two loaders
+  // (one issues about one copy in 150 cycles), MMA issuer
+  static constexpr int THREADS = 352;
+  static constexpr int LOADER = 8, ISSUER = 9, ADAPTER = 10;
   static int smem_bytes(bool cluster) {
     return STAGES * STAGE_BYTES + OP_BYTES + (cluster ? PART_BYTES : 0) + BAR_BYTES + 1024;
   }
@@ -393,25 +393,25 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
   uint64_t* full = bars;                 // [S] TMA bytes of the stage landed
   uint64_t* xfree = bars + S;            // [S] the MMAs of an X stage completed
   uint64_t* yfree = bars + 2 * S;        // [S] a Y stage's rows are stored (4 warps)
-  uint64_t* dfull = bars + 3 * S;        // [2] product ready in TMEM
-  uint64_t* dfree = bars + 3 * S + 2;    // [2] product read (4 warps)
-  uint64_t* acc_done = bars + 3 * S + 4;
-  uint64_t* op_ready = bars + 3 * S + 5;     // this CTA's rows of the operand are written
-  uint64_t* drain = bars + 3 * S + 6;
-  uint64_t* recv_ready = bars + 3 * S + 7;   // every CTA's partial of this CTA's rows is here
-  uint64_t* op_full = bars + 3 * S + 8;      // the other CTAs' rows of the operand are here
-  uint64_t* peers_done = bars + 3 * S + 9;   // every CTA has the whole operand
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 10);
+  uint64_t* dfull = bars + 3 * S;        // [ND] product ready in TMEM
+  uint64_t* dfree = dfull + C::ND;       // [ND] product read (4 warps)
+  uint64_t* acc_done = dfree + C::ND;
+  uint64_t* op_ready = acc_done + 1;         // this CTA's rows of the operand are written
+  uint64_t* drain = acc_done + 2;
+  uint64_t* recv_ready = acc_done + 3;       // every CTA's partial of this CTA's rows is here
+  uint64_t* op_full = acc_done + 4;          // the other CTAs' rows of the operand are here
+  uint64_t* peers_done = acc_done + 5;       // every CTA has the whole operand
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_done + 6);
 
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
   const int rank = (int)cluster_ctarank(), CL = (int)cluster_nctarank();
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&full[i]), 2);
       mbar_init(smem_u32(&xfree[i]), 1);
       mbar_init(smem_u32(&yfree[i]), 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::ND; ++i) {
       mbar_init(smem_u32(&dfull[i]), 1);
       mbar_init(smem_u32(&dfree[i]), 4);
     }
@@ -486,36 +486,38 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
   bool ok = true;
   if (CL > 1) cluster_arrive();        // this CTA's barriers are there for the others' arrivals
 
-  if (warp == C::LOADER) {
-    // ------------------------------------------------------------ loader
-    if (lane == 0) {
-      const uint32_t bytes = (uint32_t)(box1 - box0) * 32 * 128 + C::AD_BYTES;
-      int it = 0;
+  if (warp == C::LOADER || warp == C::ADAPTER) {
+    // ------------------------------------------------------------ loaders: rows of X and Y; the adapter
+    if (elect_one()) {
+      const bool ofrows = warp == C::LOADER;
+      const uint32_t bytes = ofrows ? (uint32_t)(box1 - box0) * 32 * 128 : C::AD_BYTES;
+      const uint32_t part = smem_u32(smem) + (ofrows ? box0 * 4096 : C::ROWS_BYTES);
+      const int y_lap = n_x / S, y_st = n_x % S;   // the first Y stage's lap of the ring and slot
+      int it = 0, st = 0, lap = 0, col = rank * 64;
       for (; it < n_x + n_y; ++it) {
-        const int st = it % S;
-        if (it >= S) {
+        if (lap > 0) {
           // the slot's last stage was an X stage (its MMAs read it) or a Y stage (stored)
-          const int prev = it - S;
-          if (prev < n_x) ok = mbar_wait(smem_u32(&xfree[st]), (prev / S) & 1, a.err);
-          else {
-            // uses of this slot by Y stages: the first is the smallest j >= n_x, j % S == st
-            const int first = n_x + ((st - n_x) % S + S) % S;
-            ok = mbar_wait(smem_u32(&yfree[st]), ((prev - first) / S) & 1, a.err);
-          }
+          const bool stored = it - S >= n_x;
+          const int uses = stored ? y_lap + (st < y_st ? 1 : 0) : 0;     // laps before the first of that kind
+          ok = mbar_wait(smem_u32(stored ? &yfree[st] : &xfree[st]), (lap - 1 - uses) & 1, a.err);
           if (!ok) break;
         }
-        uint8_t* p = smem + st * C::STAGE_BYTES;
-        const uint32_t fb = smem_u32(&full[st]), rows = smem_u32(p), adp = smem_u32(p + C::ROWS_BYTES);
+        const uint32_t dst = part + st * C::STAGE_BYTES, fb = smem_u32(&full[st]);
         mbar_arrive_expect_tx(fb, bytes);
-        if (it < n_x) {
-          const int k0 = (rank + it * CL) * C::BK;
+        if (it == n_x) col = rank * 64;
+        if (ofrows) {
+          const CUtensorMap* map = it < n_x ? &tmX : &tmY;
+          for (int b = 0; b < box1 - box0; ++b) tma_load_2d(map, fb, dst + b * 4096, col, (int)row0 + (box0 + b) * 32);
+        } else if (it < n_x) {
 #pragma unroll
-          for (int x = 0; x < C::A_ATOMS; ++x) tma_load_3d(&tmA, fb, adp + x * C::A_ATOM_BYTES, x * 64, k0, ad);
-          for (int b = box0; b < box1; ++b) tma_load_2d(&tmX, fb, rows + b * 4096, k0, (int)row0 + b * 32);
+          for (int x = 0; x < C::A_ATOMS; ++x) tma_load_3d(&tmA, fb, dst + x * C::A_ATOM_BYTES, x * 64, col, ad);
         } else {
-          const int n0 = (rank + (it - n_x) * CL) * C::BN;
-          tma_load_3d(&tmB, fb, adp, n0, 0, ad);
-          for (int b = box0; b < box1; ++b) tma_load_2d(&tmY, fb, rows + b * 4096, n0, (int)row0 + b * 32);
+          tma_load_3d(&tmB, fb, dst, col, 0, ad);
+        }
+        col += CL * 64;
+        if (++st == S) {
+          st = 0;
+          ++lap;
         }
       }
       // after a failed wait, the copies on their way land before the CTA ends
@@ -524,24 +526,29 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
     __syncwarp();
   } else if (warp == C::ISSUER) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    // (one thread's instructions set the pace of a short chain: 340 ns a stage with one loader,
+    // lane 0 and descriptors built per MMA, 190 ns with two, elected lanes and sums)
+    if (elect_one()) {
       const uint32_t id1 = idesc_bf16(128, RP, 0, 1), id2 = idesc_bf16(128, C::BN, 0, 1);
       // boxes of the operand's rows that this CTA writes, and how many come from the others
       const int b0 = rank * 4 / CL, b1 = (rank + 1) * 4 / CL;
       int theirs = 0;
       for (int b = box0; b < box1; ++b) theirs += b < b0 || b >= b1 ? 1 : 0;
       if (theirs > 0) mbar_arrive_expect_tx(smem_u32(op_full), (uint32_t)theirs * 4096 * C::OP_ATOMS);
+      // (an address counts in 16 bytes in a descriptor's low bits: stages and columns are added)
+      const uint32_t adp = smem_u32(smem) + C::ROWS_BYTES;
+      const uint64_t drows = smem_desc(smem_u32(smem), 16, 1024, kSw128), dop = smem_desc(smem_u32(op), 16, 1024, kSw128);
+      const uint64_t da = smem_desc(adp, C::A_ATOM_BYTES, 8 * C::A_ROWB, C::A_SW);
+      const uint64_t db = smem_desc(adp, RP * 128, 1024, kSw128);
       for (int it = 0; it < n_x && ok; ++it) {
         const int st = it % S;
         ok = mbar_wait(smem_u32(&full[st]), (it / S) & 1, a.err);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t rows = smem_u32(smem + st * C::STAGE_BYTES), adp = rows + C::ROWS_BYTES;
 #pragma unroll
         for (int kk = 0; kk < C::BK / 16; ++kk)
-          umma_bf16(tmem, smem_desc(rows + kk * 32, 16, 1024, kSw128),
-                    smem_desc(adp + kk * 16 * C::A_ROWB, C::A_ATOM_BYTES, 8 * C::A_ROWB, C::A_SW), id1,
-                    (it | kk) ? 1u : 0u);
+          umma_bf16(tmem, drows + (uint32_t)(st * C::STAGE_BYTES + kk * 32) / 16,
+                    da + (uint32_t)(st * C::STAGE_BYTES + kk * 16 * C::A_ROWB) / 16, id1, (it | kk) ? 1u : 0u);
         umma_commit(smem_u32(&xfree[st]));
       }
       umma_commit(smem_u32(acc_done));
@@ -563,19 +570,18 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
       }
       tc_fence_after();
       for (int j = 0; j < n_y && ok; ++j) {
-        const int it = n_x + j, st = it % S, d = j & 1;
+        const int it = n_x + j, st = it % S, d = j % C::ND;
         ok = mbar_wait(smem_u32(&full[st]), (it / S) & 1, a.err);
-        if (ok && j >= 2) ok = mbar_wait(smem_u32(&dfree[d]), ((j - 2) / 2) & 1, a.err);
+        if (ok && j >= C::ND) ok = mbar_wait(smem_u32(&dfree[d]), (j / C::ND - 1) & 1, a.err);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t adp = smem_u32(smem + st * C::STAGE_BYTES + C::ROWS_BYTES), opb = smem_u32(op);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int kk = 0; kk < RP / 16; ++kk) {
             const int col = h * RP + kk * 16;
-            umma_bf16(tmem + d * C::BN, smem_desc(opb + (col / 64) * (C::BM * 128) + (col % 64) * 2, 16, 1024, kSw128),
-                      smem_desc(adp + kk * 16 * 128, RP * 128, 1024, kSw128), id2, (h | kk) ? 1u : 0u);
+            umma_bf16(tmem + d * C::BN, dop + ((col / 64) * (C::BM * 128) + (col % 64) * 2) / 16,
+                      db + (uint32_t)(st * C::STAGE_BYTES + kk * 16 * 128) / 16, id2, (h | kk) ? 1u : 0u);
           }
         umma_commit(smem_u32(&dfull[d]));
       }
@@ -674,8 +680,8 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
     const int64_t brow = row0 + quarter * 32;              // first row of this warp's box
     const bool whole = mine && brow >= r0 && brow + 32 <= r1;
     for (int j = group; j < n_y; j += 2) {
-      const int it = n_x + j, st = it % S, d = j & 1;
-      if (ok) ok = mbar_wait(smem_u32(&dfull[d]), (j / 2) & 1, a.err);
+      const int it = n_x + j, st = it % S, d = j % C::ND;
+      if (ok) ok = mbar_wait(smem_u32(&dfull[d]), (j / C::ND) & 1, a.err);
       if (ok) ok = mbar_wait(smem_u32(&full[st]), (it / S) & 1, a.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -687,15 +693,21 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
         for (int half = 0; half < 2; ++half) {
           uint32_t v[32];
           tmem_ld32(lanes + d * C::BN + half * 32, v);
+          uint4* p[4];
+          uint4 old[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            p[g] = reinterpret_cast<uint4*>(rows + trow * 128 + (((half * 4 + g) ^ (trow & 7)) << 4));
+            old[g] = *p[g];
+          }
           tmem_wait_ld();
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            uint4* p = reinterpret_cast<uint4*>(rows + trow * 128 + (((half * 4 + g) ^ (trow & 7)) << 4));
             float y[8];
-            unpack8(*p, y);
+            unpack8(old[g], y);
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] += __uint_as_float(v[8 * g + i]);
-            *p = pack8(y);
+            *p[g] = pack8(y);
           }
         }
       }
@@ -715,6 +727,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
         if (lane == 0) mbar_arrive(smem_u32(&dfree[d]));
         if (mine) {
           // four rows at a time, eight lanes a row
+#pragma unroll 4
           for (int i = 0; i < 32; i += 4) {
             const int t = quarter * 32 + i + lane / 8, g = lane & 7, n = n0 + g * 8;
             const int64_t row = row0 + t;
