@@ -479,8 +479,16 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
   // Two cluster barriers: this CTA's barriers are set up; all that it sends is on its way, and what
-  // comes is waited for (so that CTAs end together).  Only the group that sends waits for the first.
-  if (CL > 1) cluster_arrive();
+  // comes is waited for (so that no CTA ends before).  Warps that do not send pass from the first to
+  // the second when they have time, for the last arrival takes a microsecond to be seen.
+  const auto pass = [&]() {
+    cluster_wait();
+    cluster_arrive();
+  };
+  if (CL > 1) {
+    cluster_arrive();
+    if (warp == C::ISSUER || (warp >= 4 && warp < 8)) pass();
+  }
 
   if (warp == C::LOADER || warp == C::ADAPTER) {
     // ------------------------------------------------------------ loaders: rows of X and Y; the adapter
@@ -734,10 +742,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
     __syncwarp();
   }
   if (CL > 1) {
-    if (warp >= 4) {
-      cluster_wait();
-      cluster_arrive();
-    }
+    if (warp == C::LOADER || warp == C::ADAPTER) pass();
     cluster_wait();
   }
   tc_fence_before();
