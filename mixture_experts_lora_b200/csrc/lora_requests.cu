@@ -5,7 +5,7 @@
 // prompts, by latency for a few tokens.  Two forms:
 //
 // lora_tiles_kernel, for requests of any length.  Rows are cut into windows of 128; a
-// cluster of 1 to 4 CTAs owns the rows of one request within one window and runs both
+// cluster of 1 to 8 CTAs owns the rows of one request within one window and runs both
 // products in one launch, so that X A never leaves the chip:
 //   1. X A: each CTA sums its share of K, 64 columns a stage: TMA brings the rows of X and
 //      64 rows of A, tcgen05.mma adds S[128 x RP] in TMEM;
@@ -466,8 +466,8 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
   const int nk = (a.K + C::BK - 1) / C::BK, nn = (a.N + C::BN - 1) / C::BN;
   const int n_x = (nk - rank + CL - 1) / CL;      // this CTA's stages: rank, rank + CL, ...
   const int n_y = rank < nn ? (nn - rank + CL - 1) / CL : 0;
-  // boxes with rows of the request among this CTA's 128 / CL rows
-  const int own0 = max(box0, rank * 4 / CL), own_boxes = max(0, min(box1, (rank + 1) * 4 / CL) - own0);
+  // rows in such boxes among the 128 / CL that this CTA sums up
+  const int own = C::BM / CL, own_rows = max(0, min(box1 * 32, (rank + 1) * own) - max(box0 * 32, rank * own));
 
   if (warp == C::ISSUER) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
       const uint32_t id1 = idesc_bf16(128, RP, 0, 1), id2 = idesc_bf16(128, C::BN, 0, 1);
       if (CL > 1) {
         // a row of S and a row of the operand are RP floats long, [hi | lo] in bf16
-        if (own_boxes > 0) mbar_arrive_expect_tx(smem_u32(recv_ready), (uint32_t)(CL * own_boxes) * 32 * RP * 4);
+        if (own_rows > 0) mbar_arrive_expect_tx(smem_u32(recv_ready), (uint32_t)(CL * own_rows) * RP * 4);
         mbar_arrive_expect_tx(smem_u32(op_full), (uint32_t)(box1 - box0) * 32 * RP * 4);
       }
       // (an address counts in 16 bytes in a descriptor's low bits: stages and columns are added)
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
         // Each CTA owns 128 / CL rows.  Every CTA stores its partial of them in the owner's memory
         // (row major, 16-byte pieces of row t at piece ^ t, so that rows differ in their banks) ...
         constexpr int PIECES = RP / 4;
-        const int own = C::BM / CL, owner = warp * CL / 4;
+        const int owner = tid / own;
         cluster_wait();                  // (long past: every CTA has set up its barriers)
         if (mine) {
           const uint32_t dst = mapa_smem(smem_u32(recv + (rank * own + tid % own) * RP), (uint32_t)owner);
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
         mbar_arrive(smem_u32(op_ready));
         __syncwarp();
         // ... and sums what it received for its own rows, in rank order, for all CTAs' operands
-        if (own_boxes > 0 && !mbar_wait_cluster(smem_u32(recv_ready), 0, a.err)) ok = false;
+        if (own_rows > 0 && !mbar_wait_cluster(smem_u32(recv_ready), 0, a.err)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         for (int i = tid; i < own * (RP / 8); i += C::BM) {
           const int tl = i % own, g = i / own, t = rank * own + tl;
@@ -776,20 +776,22 @@ cudaError_t launch_tiles(const LoraArgs& a, int CL, cudaStream_t s) {
   return launch_pdl(kern, dim3((unsigned)(slots * CL)), dim3(C::THREADS), smem, s, CL, tx, ta, tb, ty, a);
 }
 
-// CTAs per cluster, 1, 2 or 4: what finishes the tiles soonest if a tile takes 1 / CL and the
-// clusters that run at once are as many as measured: two CTAs per SM up to rank 32, one above, and
-// for clusters of four 33 times four CTAs on 148 SMs (clusters of 8, 15 times eight, always lost).
-// A last wave of a few clusters costs as much as a full one (rank 64, 35 tiles at 7168 x 4096:
-// 58 us with 2, 65 us with 4; rank 16, 112 tiles at 2048 x 2048: 30 us with 2, 40 us with 4), unless
-// two CTAs share an SM and it holds less than a seventh (rank 16, 67 tiles: 27.9 us with 4, 30.1 us
-// with 2, 42.6 us with 1).
+// CTAs per cluster, 1 to 8: what finishes the tiles soonest if a tile takes 1 / CL and the clusters
+// that run at once are as many as measured: two CTAs per SM up to rank 32, one above, and on 148 SMs
+// places for 33 clusters of four and 15 of eight (3 tiles, 7168 x 4096, rank 32: 14.8 us with 8, 23.2
+// with 4, 40 with 2, 70 us with 1; 20 tiles, rank 64: 38.7 us with 8, 31.0 us with 4).  A last wave of
+// a few clusters costs as much as a full one (rank 64, 35 tiles at 7168 x 4096: 53 us with 2, 61 us
+// with 4), unless two CTAs share an SM, clusters are small and it holds less than a seventh (rank 16,
+// 67 tiles at 2048 x 2048: 25.2 us with 4, 27.0 us with 2, 36.2 us with 1).
 int cluster_size(int64_t T, int S, int K, int r) {
   const double tiles = (double)((T + 127) / 128) + (S - 1);      // (requests cut windows)
   const int per_sm = r <= 32 ? 2 : 1;
   int best = 1;
   double most = 0.;
-  for (int cl = 1; cl <= 4 && cl <= (K + 63) / 64; cl *= 2) {
-    const double room = device_sms() * (cl < 4 ? 1. / cl : 2. / 9.) * per_sm;
+  for (int cl = 1; cl <= 8 && cl <= (K + 63) / 64; cl *= 2) {
+    const double places = cl < 4 ? 1. / cl : cl == 4 ? 33. / 148. : 15. / 148.;      // per SM
+    const double room = std::floor(device_sms() * places + 1e-6) * per_sm;
+    if (cl == 8 && tiles > room) break;    // (35 tiles, rank 64: 59.8 us)
     const double waves = std::ceil(tiles / room - (per_sm == 2 ? 0.15 : 0.));
     const double gain = cl / (waves < 1. ? 1. : waves);
     if (gain > most * 1.1) {               // (a cluster has its own cost)
