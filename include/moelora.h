@@ -374,7 +374,7 @@ moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int32_t n_tensors
  * [n_adapters, K, r], B bf16 [n_adapters, r, N] (an adapter of a smaller rank is padded with
  * zeros), scale fp32 [n_adapters]; seq_offsets int32 [S+1], adapters int32 [S] (device).
  * X A is summed in fp32; scale X A goes to the second product as the sum of two bf16 (or in
- * fp32 for short requests); Y is read, added to in fp32 and rounded once.
+ * fp32 in small batches); Y is read, added to in fp32 and rounded once.
  * adapters[s] >= n_adapters, or offsets that decrease or leave [0, T], set
  * MOE_ERR_DEVICE_INDEX; rows of such requests are left alone or undefined, nothing else.
  * Supported: K and N multiples of 16, 16 to 2^19; r a multiple of 8, 8 to 128; ldx >= K and

@@ -4,7 +4,7 @@
 // Reads X once, the adapters in use once, reads and writes Y once: bound by HBM for long
 // prompts, by latency for a few tokens.  Two forms:
 //
-// lora_tiles_kernel, for requests of any length.  Rows are cut into windows of 128; a
+// lora_tiles_kernel, for larger batches of requests of any length.  Rows are cut into windows of 128; a
 // cluster of 1 to 8 CTAs owns the rows of one request within one window and runs both
 // products in one launch, so that X A never leaves the chip:
 //   1. X A: each CTA sums its share of K, 64 columns a stage: TMA brings the rows of X and
@@ -23,7 +23,7 @@
 // bytes over as many SMs.  Only 32-row boxes that hold rows of the request are copied; a box
 // that it shares with another request is stored row by row.
 //
-// lora_single_kernel, for requests of a few rows: a cluster per row, see single_row.
+// lora_single_kernel, for one row per request and for small batches: a cluster per row.
 #include <climits>
 #include <cmath>
 
@@ -35,8 +35,6 @@
 namespace moe {
 namespace {
 
-// Requests of up to this many rows are worked through row by row.
-constexpr int kShortRows = 4;
 
 struct LoraArgs {
   const __nv_bfloat16* X;
@@ -51,7 +49,6 @@ struct LoraArgs {
   int n_adapters, K, N, r;
   __nv_bfloat16* Y;
   int64_t ldy;
-  int skip;                // the tiles leave requests of up to this many rows to lora_single_kernel
   int* err;
 };
 
@@ -130,7 +127,7 @@ __device__ __forceinline__ void add_scaled(float (&y)[8], uint4 w, float x) {
   for (int c = 0; c < 8; ++c) y[c] += x * v[c];
 }
 
-// Requests of one row (a cluster each), or of up to kShortRows rows (a cluster per row).
+// A cluster per row: request s is row s, or the row's request is looked up.
 __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraArgs a) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   RowSmem& sm = *reinterpret_cast<RowSmem*>(smem_raw);
@@ -144,15 +141,16 @@ __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraA
     mbar_fence_init();
   }
   pdl_begin();
-  const int unit = (int)blockIdx.x / CL, s = a.off == nullptr ? unit : unit / kShortRows;
-  const int ad = a.adapters[s];
-  int64_t row = unit;
+  const int row = (int)blockIdx.x / CL;
+  int s = row;
   if (a.off != nullptr) {
-    const int64_t lo = a.off[s], hi = a.off[s + 1];
     check_offsets(a.off, a.S, a.T, a.err);
-    row = lo + unit % kShortRows;
-    if (lo < 0 || hi > a.T || row >= hi || hi - lo > kShortRows) return;
+    s = block_count_le(a.S, row, [&](int i) { return a.off[i + 1]; });       // the first that ends past the row
+    if (s >= a.S) return;
+    const int lo = a.off[s], hi = a.off[s + 1];
+    if (row < lo || lo < 0 || hi > a.T) return;
   }
+  const int ad = a.adapters[s];
   if (ad < 0) return;                          // (the same for the cluster)
   if (ad >= a.n_adapters) {
     if (tid == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
@@ -189,7 +187,7 @@ __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraA
       met = true;
     };
     const __nv_bfloat16* A = a.A + ((int64_t)ad * a.K + k0) * r;
-    const __nv_bfloat16* X = a.X + row * a.ldx + k0;
+    const __nv_bfloat16* X = a.X + (int64_t)row * a.ldx + k0;
     const __nv_bfloat16* B = a.B + (int64_t)ad * r * a.N + (int64_t)g0 * 8;
     const int total = na + passes * nb;
     int it = 0;
@@ -271,7 +269,7 @@ __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraA
     for (int c = 0; c < 8; ++c) sm.warp[warp][g * 8 + c] = acc[c];
   }
   // the eight elements of Y that this thread finishes in a pass
-  uint4* yp = reinterpret_cast<uint4*>(a.Y + row * a.ldy) + g0 + tid;
+  uint4* yp = reinterpret_cast<uint4*>(a.Y + (int64_t)row * a.ldy) + g0 + tid;
   const auto ends = [&](int pass) { return tid < cp && g0 + pass * cp + tid < g1; };
   uint4 yv = make_uint4(0u, 0u, 0u, 0u);
   if (ends(0)) yv = *yp;
@@ -456,7 +454,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
   const int64_t w = slot - s;
   const int64_t row0 = w * C::BM;
   const int64_t r0 = row0 > lo ? row0 : lo, r1 = row0 + C::BM < hi ? row0 + C::BM : hi;
-  if (lo < 0 || r1 > a.T || r0 >= r1 || hi - lo <= a.skip || ad < 0) return;
+  if (lo < 0 || r1 > a.T || r0 >= r1 || ad < 0) return;
   if (ad >= a.n_adapters) {
     if (tid == 0) report_error(a.err, MOE_ERR_DEVICE_INDEX);
     return;
@@ -816,11 +814,20 @@ bool rows_overlap(const moe_bf16_t* x, int64_t ldx, int64_t K, const moe_bf16_t*
 // then what keeps the CTAs within two per SM (at 7168 x 2048, rank 32, with 8, 4, 2 and 1: 15 rows
 // 6.2, 7.7, 11.2, 16.9 us; 64 rows 14.4, 10.0, 11.5, 17.0 us; 128 rows 27.7, 18.7, 14.5, 17.3 us;
 // 296 rows 63, 42, 28.2, 23.5 us).
-int single_cluster(int64_t S) {
-  if (S <= 15) return 8;
+int single_cluster(int64_t rows) {
+  if (rows <= 15) return 8;
   int cl = 4;
-  while (cl > 1 && S * cl > 2 * (int64_t)device_sms()) cl /= 2;
+  while (cl > 1 && rows * cl > 2 * (int64_t)device_sms()) cl /= 2;
   return cl;
+}
+
+// Rows of a batch of packed requests up to which it is worked through row by row, each row reading
+// its adapter (rows and tiles, us: 15 rows at 7168 x 4096 7.2, 13.5 at rank 32 and 9.8, 15.1 at rank
+// 64; 64 rows 11.5, 13.4 at rank 32 and 17.7, 15.1 at rank 64).  Longer where the requests may be more
+// tiles than clusters of eight find places for (96 rows in 40 requests: 17.2, 24.7 at rank 32).
+int few_rows(int S, int r) {
+  if (S > (r <= 32 ? 30 : 15)) return 128;
+  return r <= 32 ? 64 : 24;
 }
 
 }  // namespace
@@ -862,16 +869,10 @@ extern "C" moe_status_t moe_lora_requests(const moe_bf16_t* X, int64_t ldx, cons
   a.err = moe_status_word();
   if (a.err == nullptr) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Short requests in a launch of their own where there are little else (128 requests of 128 rows
-  // in all: 21 us, 25-30 us as tiles); beside prompts they find room among the tiles (4133 rows,
-  // 35 of 40 requests of one row: 27 us, 35 us with the launch).
-  cudaError_t e = cudaSuccess;
-  if (seq_offsets == nullptr || (S >= 8 && T <= (int64_t)kShortRows * S) || T <= kShortRows) {
-    const int64_t rows = seq_offsets == nullptr ? S : (int64_t)S * kShortRows;
-    e = launch_single(a, rows, single_cluster(S), s);
-    a.skip = kShortRows;
-  }
-  if (e == cudaSuccess && seq_offsets != nullptr && T > a.skip) {
+  cudaError_t e;
+  if (seq_offsets == nullptr || T <= few_rows(S, r)) {
+    e = launch_single(a, T, single_cluster(T), s);
+  } else {
     const int cl = cluster_size(T, S, K, r);
     e = r <= 16 ? launch_tiles<16>(a, cl, s) : r <= 32 ? launch_tiles<32>(a, cl, s)
         : r <= 64 ? launch_tiles<64>(a, cl, s) : launch_tiles<128>(a, cl, s);

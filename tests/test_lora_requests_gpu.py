@@ -86,7 +86,8 @@ def test_single_tokens_over_many_buffers(T, K, N, r):
 
 
 @pytest.mark.parametrize("lens", [[1], [2], [8], [9], [15, 1], [127], [128], [129], [1, 1, 1], [0, 0, 3], [60, 1, 0, 200, 7],
-                                  [16, 16, 16, 16], [300, 1, 1, 1, 500], [1] * 40 + [100]])
+                                  [16, 16, 16, 16], [65], [33, 1, 31, 8], [16] * 6, [1] * 20 + [50], [1] * 140,
+                                  [300, 1, 1, 1, 500], [1] * 40 + [100]])
 @pytest.mark.parametrize("K,N,r", [(64, 48, 8), (320, 400, 16), (144, 656, 64)])
 def test_packed_requests(lens, K, N, r):
     off = np.cumsum([0] + lens).tolist()
