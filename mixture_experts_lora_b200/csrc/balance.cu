@@ -126,8 +126,8 @@ __device__ __forceinline__ void load_row(const float* __restrict__ px, int E, co
 }
 
 // exp(x - max) in place, 0 for -inf.  2^y to 2 ulp with y = (x - max) log2(e) rounded: a term is
-// off by |x - max| u and a few u more, u = 2^-24 (the kernel is bound by instruction issue, and
-// an exponential good to the last bit costs four times as many).
+// off by |x - max| u and a few u more, u = 2^-24 (two issue slots in three are taken, and an
+// exponential good to the last bit costs four times as many instructions).
 template <class C>
 __device__ __forceinline__ void row_exp(float (&v)[C::N], const Lanes& ln) {
   float mx = v[0];

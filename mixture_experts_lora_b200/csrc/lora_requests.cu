@@ -349,7 +349,8 @@ struct TilesCfg {
   static constexpr int ROWS_BYTES = BM * 64 * 2;          // X or Y rows of a stage
   static constexpr int AD_BYTES = RP * 64 * 2;            // A or B of a stage
   static constexpr int STAGE_BYTES = ROWS_BYTES + AD_BYTES;
-  // with a cluster's PART buffer two CTAs per SM up to rank 32
+  // two CTAs per SM up to rank 32 beside a cluster's PART buffer (a fourth stage at rank 32 would
+  // leave one), what fits above
   static constexpr int STAGES = RP == 32 || RP == 128 ? 3 : 4;
   static constexpr int OP_ATOMS = RP <= 32 ? 1 : 2 * RP / 64;   // 64-column atoms of [hi | lo]
   static constexpr int OP_BYTES = OP_ATOMS * BM * 128;
