@@ -139,6 +139,13 @@ def test_long_and_wide():
     Case(700, 7168, 2048, 32, 2, [1, 0], [0, 350, 700]).run().check()
 
 
+@pytest.mark.parametrize("T,K,N,r", [(140, 1024, 528, 128), (140, 2880, 272, 40), (300, 576, 1040, 64), (300, 528, 64, 8),
+                                     (5125, 1024, 64, 16), (5125, 256, 144, 72), (12800, 512, 64, 32), (25700, 128, 48, 16)])
+def test_tiles_over_clusters_of_every_size(T, K, N, r):
+    cut = T // 2 - 7
+    Case(T, K, N, r, 3, [2, 0, 1], [0, cut, cut + 1, T - 3]).run().check()
+
+
 def test_many_packed_requests():
     """More requests than a block has threads, most of them short, beside prompts."""
     g = torch.Generator().manual_seed(5)
