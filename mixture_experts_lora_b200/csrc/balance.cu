@@ -8,10 +8,12 @@
 //   g_s          = dloss[s] E / (k n_s^2)
 //
 // Both directions read every logit once and are bound by HBM (the backward writes as much).
-// Rows are cut into windows, a block each.  A row is spread over L lanes (a power of two, 32
-// from 128 experts on: fewer lanes leave room for several rows in a warp), each holding NQ
-// groups of V experts, V = 4 where rows are 16-byte aligned.  A warp loads U rows per lane
-// group before it works on the first, so that enough bytes are on their way.
+// Rows are cut into windows; forward a block takes the rows of one sequence in one window (131072 x
+// 128 in 64 sequences: 19.3 us; 22.2 us with a block per window, where one with rows of two
+// sequences took them one after the other), backward a window.  A row is spread over L lanes (a
+// power of two, 32 from 128 experts on: fewer lanes leave room for several rows in a warp), each
+// holding NQ groups of V experts, V = 4 where rows are 16-byte aligned.  A warp loads U rows per
+// lane group before it works on the first, so that enough bytes are on their way.
 // Forward: the lanes sum their experts' probabilities over the rows, the block's warps are
 // summed in a fixed order through shared memory, and each (window, sequence) pair writes one
 // partial row; a second launch sums a sequence's partials in a fixed order.  A batch of one
@@ -180,142 +182,140 @@ __global__ void __launch_bounds__(kThreads, C::N <= 8 ? 4 : 2) balance_partial_k
   __shared__ float s_part[kWarps];
   const int warp = warp_id(), E = a.E;
   const Lanes ln(C::LANES, a.lanes);
-  const int64_t w = blockIdx.x, t0 = w * a.rows;
-  const int64_t t1 = t0 + a.rows < a.T ? t0 + a.rows : a.T;
+  // the block's slot: rows [r0, r1) of sequence s in window w
+  const int slot = (int)blockIdx.x;
   int s = 0;
+  int64_t r0 = 0, r1 = a.T;
   if (a.off != nullptr) {
     check_offsets(a.off, a.S, a.T, a.err);
-    // (one window: every sequence's outputs are written here, the empty ones' too)
-    if (a.loss == nullptr) s = block_count_le(a.S, t0, [&](int i) { return a.off[i + 1]; });
+    s = slot;                                  // (one window: the outputs of sequence s, empty or not)
+    if (a.loss == nullptr) s = block_count_le(a.S, slot, [&](int i) { return (long long)(a.off[i] / a.rows) + i; }) - 1;
+    if (s < 0 || s > slot) return;             // (no sequence; or offsets below 0)
+    r0 = a.off[s];
+    r1 = a.off[s + 1];
   }
-  for (; s < a.S; ++s) {
-    int64_t r0 = a.off != nullptr ? a.off[s] : 0, r1 = a.off != nullptr ? a.off[s + 1] : a.T;
-    if (a.loss == nullptr && r0 >= t1) break;
-    r0 = r0 > t0 ? r0 : t0;
-    r1 = r1 < t1 ? r1 : t1;
-    if (a.loss == nullptr && r0 >= r1) {
-      // on to the first sequence that ends past this row, over any number of empty ones
-      const int to = block_count_le(a.S, r0, [&](int i) { return a.off[i + 1]; });
-      s = to - 1 > s ? to - 1 : s;
-      continue;
+  const int64_t t0 = (int64_t)(slot - s) * a.rows;
+  r0 = r0 > t0 ? r0 : t0;
+  r1 = r1 < t0 + a.rows ? r1 : t0 + a.rows;
+  if (r1 > a.T) r1 = a.T;
+  if (r0 >= r1) {
+    if (a.loss == nullptr) return;
+    r0 = r1 = 0;
+  }
+  for (int e = threadIdx.x; e < E; e += kThreads) s_cnt[e] = 0;
+  if (threadIdx.x == 0) s_n = 0;
+  __syncthreads();
+  float acc[C::N];
+#pragma unroll
+  for (int i = 0; i < C::N; ++i) acc[i] = 0.f;
+  int n = 0;
+  const int per = ln.groups * C::U;          // rows of a warp at a time
+  const int rows = (int)(r1 - r0), step = kWarps * per;
+  int t = warp * per + ln.group;             // the lane group's first row, from r0
+  const float* px = a.logits + (r0 + t) * E + ln.sub * C::V;
+  const uint8_t* pmask = a.mask != nullptr ? a.mask + r0 : nullptr;
+  // the next rows' logits are on their way while a row's softmax is computed
+  float next[C::U][C::N];
+  uint32_t next_live = 0;
+  const auto fetch = [&]() {
+    next_live = 0;
+#pragma unroll
+    for (int u = 0; u < C::U; ++u) {
+      const bool live = t + u * ln.groups < rows && (pmask == nullptr || pmask[t + u * ln.groups] != 0);
+      next_live |= (uint32_t)live << u;
+      load_row<C>(px + u * ln.groups * E, E, ln, live, next[u]);
     }
-    for (int e = threadIdx.x; e < E; e += kThreads) s_cnt[e] = 0;
-    if (threadIdx.x == 0) s_n = 0;
-    __syncthreads();
-    float acc[C::N];
+    t += step;
+    px += (int64_t)step * E;
+  };
+  // pairs per expert, eight ids on their way at a time, the first of them ahead of the logits: the
+  // counting ends while those arrive (131072 x 128, both launches: 23.7 us, 25.4 us with four
+  // ids at a time behind the logits)
+  constexpr int IDS = 8;
+  const int pairs = rows * a.k;
+  const int32_t* ids = a.ids + r0 * a.k;
+  int id[IDS];
+  uint32_t valid = 0;
+  const auto load_ids = [&](int first) {
+    valid = 0;
 #pragma unroll
-    for (int i = 0; i < C::N; ++i) acc[i] = 0.f;
-    int n = 0;
-    const int per = ln.groups * C::U;          // rows of a warp at a time
-    const int rows = (int)(r1 - r0), step = kWarps * per;
-    int t = warp * per + ln.group;             // the lane group's first row, from r0
-    const float* px = a.logits + (r0 + t) * E + ln.sub * C::V;
-    const uint8_t* pmask = a.mask != nullptr ? a.mask + r0 : nullptr;
-    // the next rows' logits are on their way while a row's softmax is computed
-    float next[C::U][C::N];
-    uint32_t next_live = 0;
-    const auto fetch = [&]() {
-      next_live = 0;
+    for (int q = 0; q < IDS; ++q) {
+      if (first + q * kThreads >= pairs) break;                // (the same for the block)
+      const int i = first + q * kThreads + threadIdx.x;
+      const bool in = i < pairs && (pmask == nullptr || pmask[(uint32_t)i / (uint32_t)a.k] != 0);
+      valid |= (uint32_t)in << q;
+      if (in) id[q] = __ldg(ids + i);
+    }
+  };
+  load_ids(0);
+  fetch();
+  for (int first = 0; first < pairs;) {
 #pragma unroll
-      for (int u = 0; u < C::U; ++u) {
-        const bool live = t + u * ln.groups < rows && (pmask == nullptr || pmask[t + u * ln.groups] != 0);
-        next_live |= (uint32_t)live << u;
-        load_row<C>(px + u * ln.groups * E, E, ln, live, next[u]);
-      }
-      t += step;
-      px += (int64_t)step * E;
-    };
-    // pairs per expert, eight ids on their way at a time, the first of them ahead of the logits: the
-    // counting ends while those arrive (131072 x 128, both launches: 23.7 us, 25.4 us with four
-    // ids at a time behind the logits)
-    constexpr int IDS = 8;
-    const int pairs = rows * a.k;
-    const int32_t* ids = a.ids + r0 * a.k;
-    int id[IDS];
-    uint32_t valid = 0;
-    const auto load_ids = [&](int first) {
-      valid = 0;
+    for (int q = 0; q < IDS; ++q) {
+      if (first + q * kThreads >= pairs) break;
+      if (((valid >> q) & 1) == 0) continue;
+      if ((uint32_t)id[q] < (uint32_t)E) atomicAdd(&s_cnt[id[q]], 1);
+      else report_error(a.err, MOE_ERR_DEVICE_INDEX);
+    }
+    first += IDS * kThreads;
+    load_ids(first);
+  }
+  for (int tw = warp * per; tw < rows; tw += step) {
+    float v[C::U][C::N];
 #pragma unroll
-      for (int q = 0; q < IDS; ++q) {
-        if (first + q * kThreads >= pairs) break;                // (the same for the block)
-        const int i = first + q * kThreads + threadIdx.x;
-        const bool in = i < pairs && (pmask == nullptr || pmask[(uint32_t)i / (uint32_t)a.k] != 0);
-        valid |= (uint32_t)in << q;
-        if (in) id[q] = __ldg(ids + i);
-      }
-    };
-    load_ids(0);
+    for (int u = 0; u < C::U; ++u)
+#pragma unroll
+      for (int i = 0; i < C::N; ++i) v[u][i] = next[u][i];
+    n += __popc(next_live);
     fetch();
-    for (int first = 0; first < pairs;) {
 #pragma unroll
-      for (int q = 0; q < IDS; ++q) {
-        if (first + q * kThreads >= pairs) break;
-        if (((valid >> q) & 1) == 0) continue;
-        if ((uint32_t)id[q] < (uint32_t)E) atomicAdd(&s_cnt[id[q]], 1);
-        else report_error(a.err, MOE_ERR_DEVICE_INDEX);
-      }
-      first += IDS * kThreads;
-      load_ids(first);
+    for (int u = 0; u < C::U; ++u) {
+      row_exp<C>(v[u], ln);
+      const float inv = row_inverse(row_sum<C>(lane_sum<C>(v[u]), ln));
+#pragma unroll
+      for (int i = 0; i < C::N; ++i) acc[i] += v[u][i] * inv;
     }
-    for (int tw = warp * per; tw < rows; tw += step) {
-      float v[C::U][C::N];
+  }
+  // rows of one warp side by side: the lanes of the same experts
+  if constexpr (!C::FULL) {
+    for (int o = ln.L; o < 32; o <<= 1) {
 #pragma unroll
-      for (int u = 0; u < C::U; ++u)
-#pragma unroll
-        for (int i = 0; i < C::N; ++i) v[u][i] = next[u][i];
-      n += __popc(next_live);
-      fetch();
-#pragma unroll
-      for (int u = 0; u < C::U; ++u) {
-        row_exp<C>(v[u], ln);
-        const float inv = row_inverse(row_sum<C>(lane_sum<C>(v[u]), ln));
-#pragma unroll
-        for (int i = 0; i < C::N; ++i) acc[i] += v[u][i] * inv;
-      }
+      for (int i = 0; i < C::N; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
     }
-    // rows of one warp side by side: the lanes of the same experts
-    if constexpr (!C::FULL) {
-      for (int o = ln.L; o < 32; o <<= 1) {
+  }
+  if (C::FULL || ln.group == 0) {
 #pragma unroll
-        for (int i = 0; i < C::N; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-      }
+    for (int q = 0; q < C::NQ; ++q) {
+      const int e = expert_of<C>(ln, q);
+#pragma unroll
+      for (int i = 0; i < C::V; ++i)
+        if (e + i < E) s_sum[warp * E + e + i] = acc[q * C::V + i];
     }
-    if (C::FULL || ln.group == 0) {
+  }
+  if (ln.sub == 0 && n > 0) atomicAdd(&s_n, n);
+  __syncthreads();
+  float part = 0.f;
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    float v = 0.f;
 #pragma unroll
-      for (int q = 0; q < C::NQ; ++q) {
-        const int e = expert_of<C>(ln, q);
-#pragma unroll
-        for (int i = 0; i < C::V; ++i)
-          if (e + i < E) s_sum[warp * E + e + i] = acc[q * C::V + i];
-      }
-    }
-    if (ln.sub == 0 && n > 0) atomicAdd(&s_n, n);
-    __syncthreads();
-    const int64_t slot = w + s;
-    float part = 0.f;
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      float v = 0.f;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) v += s_sum[i * E + e];
-      const int cnt = s_cnt[e];
-      if (a.loss != nullptr) {
-        a.out_counts[(int64_t)s * E + e] = cnt;
-        part += (float)cnt * v;
-      } else {
-        a.psum[slot * E + e] = v;
-        a.pcnt[slot * E + e] = cnt;
-      }
-    }
+    for (int i = 0; i < kWarps; ++i) v += s_sum[i * E + e];
+    const int cnt = s_cnt[e];
     if (a.loss != nullptr) {
-      const float all = block_sum(part, s_part);
-      if (threadIdx.x == 0) {
-        a.loss[s] = all * loss_factor(E, a.k, s_n);
-        a.out_n[s] = s_n;
-      }
-    } else if (threadIdx.x == 0) {
-      a.pn[slot] = s_n;
+      a.out_counts[(int64_t)s * E + e] = cnt;
+      part += (float)cnt * v;
+    } else {
+      a.psum[(int64_t)slot * E + e] = v;
+      a.pcnt[(int64_t)slot * E + e] = cnt;
     }
-    __syncthreads();
+  }
+  if (a.loss != nullptr) {
+    const float all = block_sum(part, s_part);
+    if (threadIdx.x == 0) {
+      a.loss[s] = all * loss_factor(E, a.k, s_n);
+      a.out_n[s] = s_n;
+    }
+  } else if (threadIdx.x == 0) {
+    a.pn[slot] = s_n;
   }
 }
 
@@ -585,9 +585,9 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
 
 struct Forward {
   template <class C>
-  static cudaError_t launch(const BalanceArgs& a, int64_t n_win, cudaStream_t st) {
+  static cudaError_t launch(const BalanceArgs& a, int64_t slots, cudaStream_t st) {
     ProfScope ps(K_BALANCE, st);
-    return launch_pdl(balance_partial_kernel<C>, dim3((unsigned)n_win), dim3(kThreads),
+    return launch_pdl(balance_partial_kernel<C>, dim3((unsigned)slots), dim3(kThreads),
                       (size_t)(kWarps + 1) * a.E * 4, st, 1, a);
   }
 };
@@ -601,41 +601,44 @@ struct Backward {
 
 // Four experts at a time where every row of logits (and of the gradient) is 16-byte aligned.
 template <class K>
-cudaError_t launch_rows(BalanceArgs& a, int64_t n_win, cudaStream_t s) {
+cudaError_t launch_rows(BalanceArgs& a, int64_t blocks, cudaStream_t s) {
   const bool v4 = a.E % 4 == 0 && aligned16(a.logits) && (a.dlogits == nullptr || aligned16(a.dlogits));
   const int groups = v4 ? a.E / 4 : a.E;
   a.lanes = 1;
   while (a.lanes < 32 && a.lanes < groups) a.lanes *= 2;
   const int nq = (groups + a.lanes - 1) / a.lanes;
   if (v4) {
-    if (a.lanes == 16) return K::template launch<RowCfg<4, 1, 16>>(a, n_win, s);
-    if (a.lanes == 8) return K::template launch<RowCfg<4, 1, 8>>(a, n_win, s);
-    if (a.lanes < 32) return K::template launch<RowCfg<4, 1, 0>>(a, n_win, s);
-    if (nq <= 1) return K::template launch<RowCfg<4, 1, 32>>(a, n_win, s);
-    if (nq <= 2) return K::template launch<RowCfg<4, 2, 32>>(a, n_win, s);
-    if (nq <= 4) return K::template launch<RowCfg<4, 4, 32>>(a, n_win, s);
-    return K::template launch<RowCfg<4, 8, 32>>(a, n_win, s);
+    if (a.lanes == 16) return K::template launch<RowCfg<4, 1, 16>>(a, blocks, s);
+    if (a.lanes == 8) return K::template launch<RowCfg<4, 1, 8>>(a, blocks, s);
+    if (a.lanes < 32) return K::template launch<RowCfg<4, 1, 0>>(a, blocks, s);
+    if (nq <= 1) return K::template launch<RowCfg<4, 1, 32>>(a, blocks, s);
+    if (nq <= 2) return K::template launch<RowCfg<4, 2, 32>>(a, blocks, s);
+    if (nq <= 4) return K::template launch<RowCfg<4, 4, 32>>(a, blocks, s);
+    return K::template launch<RowCfg<4, 8, 32>>(a, blocks, s);
   }
-  if (a.lanes < 32) return K::template launch<RowCfg<1, 1, 0>>(a, n_win, s);
-  if (nq <= 1) return K::template launch<RowCfg<1, 1, 32>>(a, n_win, s);
-  if (nq <= 2) return K::template launch<RowCfg<1, 2, 32>>(a, n_win, s);
-  if (nq <= 4) return K::template launch<RowCfg<1, 4, 32>>(a, n_win, s);
-  if (nq <= 8) return K::template launch<RowCfg<1, 8, 32>>(a, n_win, s);
-  if (nq <= 16) return K::template launch<RowCfg<1, 16, 32>>(a, n_win, s);
-  return K::template launch<RowCfg<1, 32, 32>>(a, n_win, s);
+  if (a.lanes < 32) return K::template launch<RowCfg<1, 1, 0>>(a, blocks, s);
+  if (nq <= 1) return K::template launch<RowCfg<1, 1, 32>>(a, blocks, s);
+  if (nq <= 2) return K::template launch<RowCfg<1, 2, 32>>(a, blocks, s);
+  if (nq <= 4) return K::template launch<RowCfg<1, 4, 32>>(a, blocks, s);
+  if (nq <= 8) return K::template launch<RowCfg<1, 8, 32>>(a, blocks, s);
+  if (nq <= 16) return K::template launch<RowCfg<1, 16, 32>>(a, blocks, s);
+  return K::template launch<RowCfg<1, 32, 32>>(a, blocks, s);
 }
 
-// Rows per window.  Batches of up to 1024 rows and 32768 logits in few sequences: one window,
-// which needs no second launch.  Otherwise about four windows per SM, two above 256 experts (a block writes, and
-// the second launch reads, a partial row per window), and 32 rows at least, less where sequences
-// are shorter (a window works through its sequences one after the other).
+// Rows of a window where `blocks` of them are to cover T: 32 at least.
+int rows_for(int64_t T, int64_t blocks) {
+  const int64_t per = (T + blocks - 1) / blocks;
+  return (int)(per < 32 ? 32 : per);
+}
+// Four blocks per SM, two above 256 experts.
+int64_t wanted_blocks(int E) { return E <= 256 ? 592 : 296; }
+// Rows per window, forward.  Batches of up to 1024 rows and 32768 logits in few sequences: one window,
+// which needs no second launch.  Otherwise as many (window, sequence) pairs as blocks are wanted
+// if sequences are few (a block writes, and the second launch reads, a partial row per pair).
 int window_rows(int64_t T, int E, int S) {
   if (T * E <= 32768 && T <= 1024 && S <= 4) return T > 0 ? (int)T : 1;
-  int64_t low = T / S;
-  low = low > 32 ? 32 : low < 8 ? 8 : low;
-  const int64_t windows = E <= 256 ? 592 : 296;
-  const int64_t per = (T + windows - 1) / windows;
-  return (int)(per < low ? low : per);
+  const int64_t blocks = wanted_blocks(E);
+  return rows_for(T, S < blocks / 2 ? blocks + 1 - S : blocks / 2);
 }
 
 moe_status_t check_shape(int64_t T, int32_t E, int32_t k, const int32_t* off, int32_t S) {
@@ -707,7 +710,7 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_ids, int6
   a.out_n = n_tokens;
   const bool one = L.n_win == 1;
   a.loss = one ? loss : nullptr;
-  if (T > 0 && launch_rows<Forward>(a, L.n_win, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (T > 0 && launch_rows<Forward>(a, L.n_win + S - 1, s) != cudaSuccess) return MOE_ERR_CUDA;
   if (!one) {
     a.loss = loss;
     ProfScope ps(K_BALANCE_SUM, s);
@@ -744,7 +747,7 @@ moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* count
   a.E = E;
   a.k = k;
   a.S = S;
-  a.rows = window_rows(T, E, S);
+  a.rows = rows_for(T, wanted_blocks(E));
   a.counts = counts;
   a.n_tokens = n_tokens;
   a.dloss = dloss;
