@@ -74,16 +74,18 @@ __device__ __forceinline__ float max_nan_abs(float a, float b) {   // a NaN wins
   return r;
 }
 
-// e4m3 code of |y|, |y| <= 448, in the top byte's low bits, from z = y 2^-120: that moves
-// e4m3's exponents to the bottom of fp32's and makes e4m3's subnormals fp32's own, after which
-// the low 20 mantissa bits are what is rounded: up if they and 20 random bits (16 and zeros)
-// carry.  The shift drops the sign.
-__device__ __forceinline__ uint32_t encode_top(float z, uint32_t rnd16) {
-  return (__float_as_uint(z) + rnd16 * 16u) << 4;
+// e4m3 code of |y|, |y| <= 448, in bits 20 to 27 (and y's sign in bit 31), from z = y 2^-120: that
+// moves e4m3's exponents to the bottom of fp32's and makes e4m3's subnormals fp32's own, after
+// which the low 20 mantissa bits are what is rounded: up if they and 20 random bits (16 and zeros)
+// carry.
+__device__ __forceinline__ uint32_t encode_bits(float z, uint32_t rnd16) {
+  return __float_as_uint(z) + rnd16 * 16u;
 }
-// The top bytes of four words.
-__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+// The codes of four such words as four bytes, and bytes with their signs in bit 7.
+__device__ __forceinline__ uint32_t code_bytes(const uint32_t (&t)[4], uint32_t& signs) {
+  const uint32_t lo = __byte_perm(t[0], t[1], 0x7632), hi = __byte_perm(t[2], t[3], 0x7632);
+  signs = __byte_perm(lo, hi, 0x7531);
+  return __byte_perm(lo << 4, hi << 4, 0x7531);
 }
 // 0x80 in every byte that is not zero (bytes up to 0x80).
 __device__ __forceinline__ uint32_t nonzero_bytes(uint32_t w) { return (w + 0x7f7f7f7fu) & 0x80808080u; }
@@ -269,16 +271,15 @@ __device__ __forceinline__ void encode_block(const float (&m)[8], const float (&
           y = x ^ (x >> 16);
         }
         const uint32_t h = mix_end(y), hi = h >> 16;
-        tm[i + e] = encode_top(e ? zm.y : zm.x, (h ^ hi) & 0xffffu);
-        tv[i + e] = encode_top(e ? zv.y : zv.x, hi);
+        tm[i + e] = encode_bits(e ? zm.y : zm.x, (h ^ hi) & 0xffffu);
+        tv[i + e] = encode_bits(e ? zv.y : zv.x, hi);
       }
     }
-    wm[k] = top_bytes(tm[0], tm[1], tm[2], tm[3]);
-    const uint32_t sign = top_bytes(__float_as_uint(m[4 * k]), __float_as_uint(m[4 * k + 1]),
-                                    __float_as_uint(m[4 * k + 2]), __float_as_uint(m[4 * k + 3]));
+    uint32_t sign, none;
+    wm[k] = code_bytes(tm, sign);
     wm[k] |= sign & nonzero_bytes(wm[k]);              // (zero has no sign)
     // a positive root is never stored as zero
-    wv[k] = top_bytes(tv[0], tv[1], tv[2], tv[3]);
+    wv[k] = code_bytes(tv, none);
     uint32_t least = 0x01010101u;
     if (!normal) {
       least = 0;
