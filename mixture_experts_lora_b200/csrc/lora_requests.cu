@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraA
       const uint32_t bar = smem_u32(&sm.full[st]), dst = smem_u32(sm.slot[st]);
       if (it < na) {
         const int o = it * rows_c, n = k1 - k0 - o < rows_c ? k1 - k0 - o : rows_c;
-        if (lane == 0) {
+        if (elect_one()) {
           mbar_arrive_expect_tx(bar, (uint32_t)n * (r * 2 + 2));
           bulk_load(dst, A + (int64_t)o * r, (uint32_t)n * r * 2, bar);
           bulk_load(dst + kSlotBytes, X + o, (uint32_t)n * 2, bar);
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraA
         const int p = (it - na) / nb, j0 = (it - na) % nb * rb;
         const int seg = g1 - g0 - p * cp < cp ? g1 - g0 - p * cp : cp;
         const int n = r - j0 < rb ? r - j0 : rb;
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * seg) * 16);
+        if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(n * seg) * 16);
         __syncwarp();
         for (int j = lane; j < n; j += 32)
           bulk_load(dst + j * cp * 16, B + (int64_t)(j0 + j) * a.N + (int64_t)p * cp * 8, (uint32_t)seg * 16, bar);
