@@ -374,8 +374,8 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
                       const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmY,
                       const LoraArgs a) {
   constexpr int RP = C::RP, S = C::STAGES;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_tiles[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_tiles) + 1023) & ~uintptr_t(1023));
   uint8_t* op = smem + S * C::STAGE_BYTES;                 // [hi | lo] operand of the second product
   uint64_t* bars = reinterpret_cast<uint64_t*>(op + C::OP_BYTES);
   float* recv = reinterpret_cast<float*>(op + C::OP_BYTES + C::BAR_BYTES);   // clusters only
