@@ -406,7 +406,9 @@ __device__ __forceinline__ void bulk_wait() {
 // set-up, TMEM allocation, descriptor prefetch - overlaps that tail).  pdl_wait()
 // blocks until the predecessors have completed and their writes are visible; each
 // kernel calls it before its first global-memory access, read or write, and then
-// lets its own dependents be scheduled.
+// lets its own dependents be scheduled.  A kernel that takes TMEM holds its columns before
+// it lets them in: a dependent may take columns on the same SM and then wait for this grid
+// to end, so an allocation of this grid behind it could wait for ever.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -414,7 +414,9 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmY);
   }
-  pdl_begin();
+  // (The dependents are let in only when this CTA holds its TMEM columns, below: other kernels take theirs
+  // before they wait for this grid to end, and would then wait for each other.)
+  pdl_wait();
   check_offsets(a.off, a.S, a.T, a.err);
   // the cluster's tile, the same for all its CTAs: slot -> (window, request) -> rows, adapter
   const int slot = (int)blockIdx.x / CL;
@@ -471,6 +473,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
   // Two cluster barriers: this CTA's barriers are set up; all that it sends is on its way, and what
