@@ -730,6 +730,7 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
               *reinterpret_cast<uint4*>(a.Y + row * a.ldy + n) =
                   *reinterpret_cast<const uint4*>(rows + t * 128 + ((g ^ (t & 7)) << 4));
           }
+          fence_proxy_async_smem();        // (the slot's next bytes come by a bulk copy)
           __syncwarp();
         }
         if (lane == 0) mbar_arrive(smem_u32(&yfree[st]));

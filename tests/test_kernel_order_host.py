@@ -42,3 +42,12 @@ def test_dependents_are_let_in_once_tmem_is_held(f, name, body):
     let = [m.start() for m in re.finditer(r"\b(pdl_begin|pdl_launch_dependents)\(", body)]
     assert len(let) == 1, f"{f}: {name}"
     assert all(t < let[0] for t in take), f"{f}: {name}"
+
+
+def test_shared_memory_stores_are_fenced_before_a_bulk_copy_overwrites_them():
+    """lora_tiles_kernel: the warps that have stored into a slot of rows hand it to the loader, whose copy
+    goes through another proxy: a fence stands between, in every branch."""
+    body = next(b for _, n, b in KERNELS if n == "lora_tiles_kernel")
+    parts = body[body.index("= pack8(y)"):].split("mbar_arrive(smem_u32(&yfree[st]))")
+    assert len(parts) == 3
+    assert all("fence_proxy_async_smem()" in p for p in parts[:2])

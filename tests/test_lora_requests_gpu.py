@@ -274,3 +274,16 @@ def test_refusals():
     for kw in (dict(X=z(4, 66)[:, 2:]), dict(Y=z(4, 36)[:, :32]), dict(A=z(2, 64, 12), B=z(2, 12, 32))):
         with pytest.raises(ml.MoEError):
             ml.moe_lora_requests(**{**ok, **kw})
+
+
+@pytest.mark.parametrize("K,N,r,lens", [(64, 8208, 16, [45, 90, 77, 1, 130]), (192, 4112, 32, [33, 31, 95, 200, 14]),
+                                        (128, 4112, 128, [130, 50, 100]), (2048, 4096, 64, [100, 300, 259])])
+def test_ragged_edges_over_many_column_stages(K, N, r, lens):
+    """Every request begins and ends inside a box of rows, whose slots are used again and again: every
+    run gives the same bits."""
+    off = np.cumsum([3] + lens).tolist()
+    make = lambda: Case(off[-1] + 5, K, N, r, 3, [i % 3 for i in range(len(lens))], off, seed=K)      # noqa: E731
+    want = make().run()
+    want.check()
+    for _ in range(8):
+        assert torch.equal(make().run().Y, want.Y)
