@@ -353,6 +353,11 @@ struct TilesCfg {
   static constexpr int PART_BYTES = BM * RP * 4;          // exchanged partial (clusters only)
   static constexpr int BAR_BYTES = 256;
   static constexpr int ND = 4, TMEM_COLS = ND * 64;       // accumulators of 64 columns; S before them
+  // S as the sum of NS accumulators that the stages take in turn: the tensor cores cut off what lies
+  // below an accumulator's last bits instead of rounding it, an error of one sign that grows with the
+  // accumulator and with the length of its chain (16384 products of one sign: 8.2e-5 of the sum in
+  // one chain, 1.4e-5 in four; 16384 rows at 7168 x 4096, rank 32: 100 us both ways)
+  static constexpr int NS = RP == 128 ? 2 : 4;
   // two groups of four epilogue warps (the second stage by stage in turn with the first), two loaders
   // (one issues about one copy in 150 cycles), MMA issuer
   static constexpr int THREADS = 352;
@@ -549,8 +554,8 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < C::BK / 16; ++kk)
-          umma_bf16(tmem, drows + (uint32_t)(st * C::STAGE_BYTES + kk * 32) / 16,
-                    da + (uint32_t)(st * C::STAGE_BYTES + kk * 16 * C::A_ROWB) / 16, id1, (it | kk) ? 1u : 0u);
+          umma_bf16(tmem + it % C::NS * RP, drows + (uint32_t)(st * C::STAGE_BYTES + kk * 32) / 16,
+                    da + (uint32_t)(st * C::STAGE_BYTES + kk * 16 * C::A_ROWB) / 16, id1, it >= C::NS || kk ? 1u : 0u);
         umma_commit(smem_u32(&xfree[st]));
       }
       umma_commit(smem_u32(acc_done));
@@ -592,6 +597,22 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const float c = a.scale[ad];
+      // 16 columns of S from c0 on: the accumulators in use, summed in fp32
+      const auto load_s = [&](int c0, float (&x)[16]) {
+        uint32_t v[16];
+        tmem_ld16(lanes + c0, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
+#pragma unroll
+        for (int q = 1; q < C::NS; ++q) {
+          if (q >= n_x) break;
+          tmem_ld16(lanes + q * RP + c0, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] += __uint_as_float(v[i]);
+        }
+      };
       // c S of a row's eight columns from c0 on, split into two bf16: pieces of an operand row
       const auto write_op = [&](int t, int c0, const float (&x)[8], auto&& store) {
         float h[8], l[8];
@@ -610,14 +631,13 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
       if (CL == 1) {
 #pragma unroll 1
         for (int c0 = 0; c0 < RP; c0 += 16) {
-          uint32_t v[16];
-          tmem_ld16(lanes + c0, v);
-          tmem_wait_ld();
+          float v[16];
+          load_s(c0, v);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * g + i]);
+            for (int i = 0; i < 8; ++i) x[i] = v[8 * g + i];
             write_op(tid, c0 + 8 * g, x, [](uint8_t* at, uint4 v) { *reinterpret_cast<uint4*>(at) = v; });
           }
         }
@@ -635,13 +655,13 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
           const uint32_t bar = mapa_smem(smem_u32(recv_ready), (uint32_t)owner);
 #pragma unroll
           for (int c0 = 0; c0 < RP; c0 += 16) {
-            uint32_t v[16];
-            tmem_ld16(lanes + c0, v);
-            tmem_wait_ld();
+            float v[16];
+            load_s(c0, v);
 #pragma unroll
             for (int g = 0; g < 4; ++g)
               st_async_u4(dst + ((c0 / 4 + g) ^ (tid & (PIECES - 1))) * 16,
-                          make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]), bar);
+                          make_uint4(__float_as_uint(v[4 * g]), __float_as_uint(v[4 * g + 1]),
+                                     __float_as_uint(v[4 * g + 2]), __float_as_uint(v[4 * g + 3])), bar);
           }
         }
         tc_fence_before();

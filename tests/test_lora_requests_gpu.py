@@ -287,3 +287,32 @@ def test_ragged_edges_over_many_column_stages(K, N, r, lens):
     want.check()
     for _ in range(8):
         assert torch.equal(make().run().Y, want.Y)
+
+
+@pytest.mark.parametrize("tiles,K,r", [(148, 16384, 64), (296, 16384, 16), (148, 16384, 128), (1, 65536, 32)])
+def test_long_sums_keep_their_digits(tiles, K, r):
+    """X A over many columns, all of one sign, B the identity and Y the negative of the rounded result,
+    so that Y ends as what the rounding left, a few digits of which show the sum's own error.
+
+    Bound, of the sum: an instruction adds 16 products to an accumulator and cuts off less than a unit
+    in its last place, 2^-23, at most twice (aligning the summands, and the result).  A sum runs through
+    2 accumulators or more, K / 32 instructions; at ranks up to 64 through 4, K / 64.  Four fp32 additions
+    and the scale, 2^-24 each; c X A as two bf16, 2^-17; and Y's own rounding, 2^-9 of what is left."""
+    T, N = 128 * tiles, 16 * ((r + 15) // 16)
+    g = torch.Generator(device="cuda").manual_seed(K + r)
+    X = torch.randn(T, K, generator=g, device="cuda").to(BF).abs_()
+    A = torch.randn(1, K, r, generator=g, device="cuda").to(BF).abs_()
+    B = torch.zeros(1, r, N, device="cuda")
+    B[0, :, :r] = torch.eye(r, device="cuda")
+    ref = torch.zeros(T, N, dtype=torch.float64, device="cuda")
+    for i in range(0, T, 2048):
+        ref[i:i + 2048, :r] = X[i:i + 2048].double() @ A[0].double()
+    Y = -ref.to(BF)
+    want = Y.double() + ref
+    ml.moe_lora_requests(X, torch.zeros(1, dtype=torch.int32, device="cuda"), A, B.to(BF), torch.ones(1, device="cuda"),
+                         Y, torch.tensor([0, T], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert ml.moe_get_device_error() == ml.MOE_OK
+    chain = K / (32 if r > 64 else 64)
+    tol = (chain * 2.0 ** -22 + 5 * U + 2.0 ** -17) * ref + 2.0 ** -9 * want.abs()
+    assert ((Y.double() - want).abs() <= tol).all()
