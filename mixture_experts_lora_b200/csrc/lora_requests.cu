@@ -618,7 +618,8 @@ __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
         float h[8], l[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float v = x[i] * c;
+          // (ranks past r are zeros of A and B; a row that is not finite would bring 0 x inf into them)
+          const float v = c0 < a.r ? x[i] * c : 0.f;
           h[i] = __bfloat162float(__float2bfloat16_rn(v));
           l[i] = isinf(h[i]) ? 0.f : v - h[i];
         }

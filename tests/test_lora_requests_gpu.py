@@ -316,3 +316,17 @@ def test_long_sums_keep_their_digits(tiles, K, r):
     chain = K / (32 if r > 64 else 64)
     tol = (chain * 2.0 ** -22 + 5 * U + 2.0 ** -17) * ref + 2.0 ** -9 * want.abs()
     assert ((Y.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("r", [8, 16, 24, 40, 64, 72])
+@pytest.mark.parametrize("off", [None, [0, 140, 200]])
+def test_infinite_rows_follow_the_definition(off, r):
+    """An infinity in X times positive adapters is an infinity in every entry, whatever the rank."""
+    c = Case(200, 256, 96, r, 1, [0] * (200 if off is None else 2), off)
+    c.A.abs_()
+    c.B.abs_()
+    c.Xs[17, 3], c.Xs[150, 200] = float("inf"), -float("inf")
+    c.run()
+    assert (c.Y[17] == float("inf")).all() and (c.Y[150] == -float("inf")).all()
+    rest = [i for i in range(200) if i not in (17, 150)]
+    assert torch.isfinite(c.Y[rest]).all()
