@@ -158,10 +158,11 @@ __device__ __forceinline__ void weight(const Step& q, float m, float root, float
   w = w * q.keep - q.c1 * (m * rcp_approx(root * q.rbc2 + q.eps));
 }
 
-// Eight elements two at a time: m, v, sqrt(v), w from m, v, g, w.  Returns whether every v is a
-// normal number.  The root of a normal v is one Newton step (v - s^2) / (2 s) from
+// Eight elements two at a time: m, v, sqrt(v), w from m, v, g, w.  Returns whether every v is
+// finite and at least 2^-100.  Their roots are one Newton step (v - s^2) / (2 s) from
 // s = v rsqrt(v): equal to __fsqrt_rn for all 2^24 values of [1, 4), and so for their scalings
-// by 4^k, in half its instructions (the 8-bit step is bound by instruction issue).
+// by 4^k down to 2^-100 (below 2^-102 the bits of v - s^2 leave fp32's range), in half its
+// instructions (the 8-bit step is bound by instruction issue).
 __device__ __forceinline__ bool update8(const Step& q, const float (&g)[8], float (&m)[8], float (&v)[8],
                                         float (&u)[8], float (&w)[8]) {
   const f32x2 b1 = pack2(q.b1, q.b1), b2 = pack2(q.b2, q.b2), o1 = pack2(q.one_b1, q.one_b1),
@@ -184,7 +185,7 @@ __device__ __forceinline__ bool update8(const Step& q, const float (&g)[8], floa
     low = min(low, __float_as_uint(v[j]));
     high = max(high, __float_as_uint(v[j]));
   }
-  const bool normal = low >= 0x00800000u && high < 0x7f800000u;
+  const bool normal = low >= 0x0d800000u && high < 0x7f800000u;
   if (normal) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -230,7 +231,7 @@ __device__ __forceinline__ void decode_v(uint2 c, float scale, float (&v)[8]) {
 }
 
 // The codes of a warp's block of 256 elements and its scales.  Lane's elements: index, index +
-// step, ...; normal: all its v are normal numbers.
+// step, ...; normal: all its v are positive and finite.
 __device__ __forceinline__ void encode_block(const float (&m)[8], const float (&v)[8], const float (&u)[8],
                                              uint32_t index, uint32_t step, uint32_t seed, bool normal,
                                              uint2& cm, uint2& cv, float& ms, float& vs) {

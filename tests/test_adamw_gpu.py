@@ -366,3 +366,42 @@ def test_elements_past_32_bits(bits):
     torch.cuda.synchronize()
     assert torch.equal(p[-tail:], sp)
     assert not p[:-tail].any()
+
+
+@pytest.mark.parametrize("e", [-126, -125, -120, -110, -103, -101, -100, -99, -80, -1, 0])
+def test_the_root_of_small_moments(e):
+    """Groups of eight and single elements take the same root: with w = 0 and eps = 0 the weight shows it
+    to the last bits.  v from 2^e up to twice that; both forms round every operation alike."""
+    n = 4096
+    g = torch.Generator(device="cuda").manual_seed(e + 200)
+    v = torch.ldexp(torch.rand(n, generator=g, device="cuda") + 1.0, torch.tensor(e + 1.0, device="cuda"))
+    m = torch.sqrt(v) * (torch.rand(n, generator=g, device="cuda") + 0.5)
+    out = []
+    for offset in (0, 1):                    # aligned: groups of eight; one off: single elements
+        p = torch.zeros(n + offset, device="cuda")[offset:]
+        opt = ml.AdamW([p], [torch.zeros(n + offset, device="cuda")[offset:]], lr=1.0, betas=(0.5, 0.5), eps=0.0,
+                       weight_decay=0.0)
+        opt.exp_avg.copy_(m)
+        opt.exp_avg_sq.copy_(v)
+        opt.step()
+        assert torch.equal(opt.exp_avg_sq, v / 2) and torch.equal(opt.exp_avg, m / 2)
+        out.append(p)
+    assert torch.equal(out[0], out[1])
+
+
+def test_the_root_of_every_moment_of_two_octaves():
+    """All 2^24 floats of [1, 4) as v, groups of eight against single elements."""
+    n = 1 << 24
+    v = (torch.arange(n, dtype=torch.int32, device="cuda") + 0x3F800000).view(torch.float32)
+    assert v[0] == 1 and v[-1] < 4 and v[-1] > 3.9999995
+    out = []
+    for offset in (0, 1):
+        p = torch.zeros(n + offset, device="cuda")[offset:]
+        opt = ml.AdamW([p], [torch.zeros(n + offset, device="cuda")[offset:]], lr=1.0, betas=(0.5, 0.5), eps=0.0,
+                       weight_decay=0.0)
+        opt.exp_avg.copy_(v.flip(0))
+        opt.exp_avg_sq.copy_(v * 2)
+        opt.step()
+        assert torch.equal(opt.exp_avg_sq, v)
+        out.append(p)
+    assert torch.equal(out[0], out[1])
