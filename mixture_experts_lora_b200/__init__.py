@@ -10,6 +10,7 @@ or was not built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import os
 from dataclasses import dataclass
 
@@ -407,6 +408,8 @@ def moe_lora_requests(X, adapters, A, B, scale, Y, seq_offsets=None, stream=None
 
 # ---------------------------------------------------------------- AdamW
 STATE_BLOCK = 256     # elements that share a scale in 8-bit states
+LOOKED_AT = 32        # tensors whose addresses one step compares (50 ns each; a step's own host time is 5 us)
+_data_ptr = torch.Tensor.data_ptr
 
 
 def _joint_view(p, g):
@@ -442,7 +445,13 @@ class AdamW:
     states live in flat tensors, each parameter's part beginning at a multiple of 256 elements
     (`starts`): exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale (8 bits), master.  steps is
     the number of steps taken, a device int64 that step() moves on, so that a captured step
-    counts too.  Steps of one optimizer must be ordered on the device."""
+    counts too.  Steps of one optimizer must be ordered on the device.
+
+    The parameters and gradients must keep their memory, and their sizes and strides, while the
+    optimizer is in use: steps, captured ones too, go to the addresses of its construction, whose
+    storage it keeps alive.  step() raises ValueError, without a launch, when it sees a tensor that has
+    been given other memory (`p.data = ...`, a module's cast or move); it looks at 32 of them, the next
+    ones each time where there are more."""
 
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
                  state_bits: int = 32, master_weights: bool = False):
@@ -491,6 +500,11 @@ class AdamW:
             self.master = torch.zeros(at, dtype=torch.float32, device=dev)
             for i in (i for g, idx in groups.items() if g[2] for i in idx):
                 self._part(self.master, i).copy_(self.params[i])
+        tensors = self.params + self.grads
+        self._held = [t.detach() for t in tensors]
+        self._looks = [(ts, list(map(_data_ptr, ts)))
+                       for ts in (tensors[i:i + LOOKED_AT] for i in range(0, len(tensors), LOOKED_AT))]
+        self._next_look = itertools.cycle(self._looks).__next__
         self._count = torch.zeros(2, dtype=torch.int64, device=dev)
         self._count_ptr = self._count.data_ptr()
         self.steps = self._count[0]
@@ -520,6 +534,9 @@ class AdamW:
     def step(self, grad_scale=None, stream=None):
         """One step with the gradients in the buffers, times grad_scale (a device fp32 tensor of
         one element) where given."""
+        tensors, addresses = self._next_look()
+        if list(map(_data_ptr, tensors)) != addresses:
+            self._moved()
         lr, scale = self.lr, None
         lr_dev = None
         if isinstance(lr, torch.Tensor):
@@ -531,6 +548,10 @@ class AdamW:
         for table, n, cfg, ref, last in self._calls:
             cfg.lr = lr
             _launch("moe_adamw_step", self.index, stream, table, n, ref, lr_dev, scale, self._count_ptr, last)
+
+    def _moved(self):
+        raise ValueError("a parameter or gradient has been given other memory since this optimizer was made: "
+                         "make a new one over the tensors as they are now")
 
     def _scalar(self, name, t):
         if t.dtype is not _F32 or t.numel() != 1 or t.get_device() != self.index:
@@ -557,6 +578,8 @@ class AdamW:
 
     def load_state_dict(self, state: dict):
         """Copies a state_dict() of an optimizer over the same parameters and settings."""
+        if any(list(map(_data_ptr, tensors)) != addresses for tensors, addresses in self._looks):
+            self._moved()
         for k in self._STATE:
             mine, other = getattr(self, k), state[k]
             if (mine is None) != (other is None) or (mine is not None and (mine.shape != other.shape

@@ -405,3 +405,36 @@ def test_the_root_of_every_moment_of_two_octaves():
         assert torch.equal(opt.exp_avg_sq, v)
         out.append(p)
     assert torch.equal(out[0], out[1])
+
+
+@pytest.mark.parametrize("which", ["params", "grads"])
+def test_tensors_that_were_given_other_memory(which):
+    opt = make([(40,), (3, 70), (513,)], F32, F32)
+    for g in opt.grads:
+        g.fill_(1.0)
+    opt.step()
+    t = getattr(opt, which)[1]
+    old = t.detach()
+    before = [p.clone() for p in opt.params]
+    t.data = t.detach().clone()
+    for call in (opt.step, lambda: opt.load_state_dict(opt.state_dict())):
+        with pytest.raises(ValueError):
+            call()
+    assert int(opt.steps) == 1 and all(torch.equal(p, b) for p, b in zip(opt.params, before))
+    t.data = old
+    opt.step()
+    assert int(opt.steps) == 2 and not torch.equal(opt.params[1], before[1])
+
+
+def test_other_memory_is_seen_among_many_tensors():
+    """Where a step does not look at all tensors, the next ones do; meanwhile the old memory is kept."""
+    opt = make([(10 + i,) for i in range(100)], F32, F32)
+    at = opt.params[70].data_ptr()
+    opt.params[70].data = opt.params[70].clone()
+    junk = [torch.zeros(80, device="cuda") for _ in range(50)]
+    assert all(j.data_ptr() != at for j in junk)
+    with pytest.raises(ValueError):
+        for _ in range(-(-200 // ml.LOOKED_AT)):
+            opt.step()
+    torch.cuda.synchronize()
+    assert not any(j.any() for j in junk)
