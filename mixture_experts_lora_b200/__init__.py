@@ -431,6 +431,38 @@ def _joint_view(p, g):
     return [(1, 0, 0)] * (3 - len(out)) + out
 
 
+def _need_apart(params):
+    """ValueError where two parameters share an element's memory."""
+    spans = []
+    for i, p in enumerate(params):
+        if p.numel():
+            last = sum((n - 1) * st for n, st in zip(p.shape, p.stride()))
+            spans.append((p.data_ptr(), p.data_ptr() + (last + 1) * p.element_size(), i))
+    spans.sort()
+    at = 0
+    while at < len(spans):                # runs of spans that meet
+        lo, hi, end = spans[at][0], spans[at][1], at + 1
+        while end < len(spans) and spans[end][0] < hi:
+            hi = max(hi, spans[end][1])
+            end += 1
+        run, at = [i for _, _, i in spans[at:end]], end
+        if len(run) == 1:
+            continue
+        # interleaved views: their elements are marked one tensor after the other, in units of two bytes
+        taken = None
+        if not all(params[i].is_contiguous() for i in run):
+            taken = torch.zeros((hi - lo) // 2, dtype=torch.bool, device=params[run[0]].device)
+        for i in run:
+            p = params[i]
+            if taken is not None:
+                u = p.element_size() // 2
+                mine = taken.as_strided((*p.shape, u), (*(s * u for s in p.stride()), 1), (p.data_ptr() - lo) // 2)
+                if not mine.any():
+                    mine.fill_(True)
+                    continue
+            raise ValueError(f"parameter {i} shares memory with another one (of parameters {run})")
+
+
 class AdamW:
     """AdamW over many tensors in one launch (moe_adamw_step), e.g. the adapters of all layers.
 
@@ -464,7 +496,7 @@ class AdamW:
         self.index = _index_of("parameters", self.params[0])
         self.lr, self.state_bits = lr, state_bits
         ok = (torch.bfloat16, torch.float32)
-        groups, taken, at = {}, set(), 0
+        groups, at = {}, 0
         self.starts, views = [], []
         for i, (p, g) in enumerate(zip(self.params, self.grads)):
             if p.dtype not in ok or g.dtype not in ok or p.shape != g.shape or p.device != dev or g.device != dev:
@@ -476,9 +508,6 @@ class AdamW:
                     if sp < reach:
                         raise ValueError(f"parameter {i} has several elements in one place")
                     reach = sp * (n - 1) + reach
-            if p.numel() and p.data_ptr() in taken:
-                raise ValueError(f"parameter {i} begins where another one does")
-            taken.add(p.data_ptr())
             if any(v[0] > 1 for v in view[:2]) and p.numel() >= 1 << 31:
                 raise ValueError(f"parameter {i}: a strided view holds fewer than 2^31 elements")
             views.append(view)
@@ -486,6 +515,7 @@ class AdamW:
             at += -(-p.numel() // STATE_BLOCK) * STATE_BLOCK
             with_master = master_weights and p.dtype == torch.bfloat16
             groups.setdefault((p.dtype == torch.bfloat16, g.dtype == torch.bfloat16, with_master), []).append(i)
+        _need_apart(self.params)
         if state_bits == 8:
             self.exp_avg = torch.zeros(at, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
             self.exp_avg_sq = torch.zeros(at, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)

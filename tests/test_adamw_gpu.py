@@ -438,3 +438,20 @@ def test_other_memory_is_seen_among_many_tensors():
             opt.step()
     torch.cuda.synchronize()
     assert not any(j.any() for j in junk)
+
+
+def test_parameters_that_share_memory_are_refused():
+    flat = torch.zeros(400, device="cuda")
+    grid = torch.zeros(6, 20, 32, device="cuda", dtype=BF)
+    def make_over(*params):
+        return ml.AdamW(list(params), [torch.zeros(p.shape, dtype=p.dtype, device="cuda") for p in params], **H)
+    for bad in ((flat[0:10], flat[5:15]), (flat[5:15], flat[0:300], flat[390:]), (flat[:10], flat[9:10]),
+                (grid[:, :, :16], grid[:, :, 15:]), (grid[:, :8], grid), (grid[:, ::2, :8], grid[:, 1:19, 4:20]),
+                (flat[::2], flat[2:3]), (flat[:100].view(torch.bfloat16), flat[99:120]),
+                (flat[::4], flat[1::4], flat[2::4], flat[6::4])):
+        with pytest.raises(ValueError):
+            make_over(*bad)
+    for good in ((flat[0:10], flat[10:15]), (grid[:, :, :16], grid[:, :, 16:]), (grid[:, ::2, :16], grid[:, 1::2], grid[:, ::2, 16:]),
+                 (flat[::2], flat[1::2]), (flat[:100].view(torch.bfloat16), flat[100:120]), (flat[5:5], flat[0:10], flat[5:5]),
+                 (flat[::4], flat[1::4], flat[2::4], flat[3::4])):
+        steps(make_over(*good), n=1)
