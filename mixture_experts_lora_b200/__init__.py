@@ -9,6 +9,7 @@ or was not built, every call raises.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import itertools
 import os
@@ -535,6 +536,7 @@ class AdamW:
         self._looks = [(ts, list(map(_data_ptr, ts)))
                        for ts in (tensors[i:i + LOOKED_AT] for i in range(0, len(tensors), LOOKED_AT))]
         self._next_look = itertools.cycle(self._looks).__next__
+        self._by_address = sorted((p.data_ptr(), i) for i, p in enumerate(self.params) if p.numel())
         self._count = torch.zeros(2, dtype=torch.int64, device=dev)
         self._count_ptr = self._count.data_ptr()
         self.steps = self._count[0]
@@ -578,6 +580,22 @@ class AdamW:
         for table, n, cfg, ref, last in self._calls:
             cfg.lr = lr
             _launch("moe_adamw_step", self.index, stream, table, n, ref, lr_dev, scale, self._count_ptr, last)
+
+    def _check_gradients(self, pairs):
+        """For pairs (weights, gradient of the same shape): ValueError unless this optimizer holds some of the
+        weights, or views of them, each with the same place of the gradient as its buffer."""
+        any_held = False
+        for w, g in pairs:
+            lo = w.data_ptr()
+            for at, i in self._by_address[bisect.bisect_left(self._by_address, (lo, -1)):]:
+                if at >= lo + w.nbytes:
+                    break
+                any_held = True
+                if self.grads[i].data_ptr() != g.data_ptr() + (at - lo) // w.element_size() * g.element_size():
+                    raise ValueError(f"the optimizer's gradient of parameter {i} is not the buffer that the layer's "
+                                     "backward writes")
+        if not any_held:
+            raise ValueError("the optimizer holds none of the layer's adapters")
 
     def _moved(self):
         raise ValueError("a parameter or gradient has been given other memory since this optimizer was made: "
@@ -753,9 +771,12 @@ def layer_train_step(inp: dict, k: int, scale: float, buf: LayerBuffers, opt: Ad
                      balance: BalanceBuffers | None = None, seq_offsets=None, token_mask=None, group=None,
                      grad_scale=None, stream=None):
     """One training step of the layer: forward, backward against inp['dY'], the adapter gradients
-    summed over the data-parallel ranks, and the optimizer's step (opt holds the layer's adapters
-    and buf's gradient buffers).  With `balance` the router's gradient comes too: balance.dlogits
+    summed over the data-parallel ranks, and the optimizer's step (opt holds the layer's adapters,
+    or some of them or views, with buf's gradient buffers or the same views of those; it may hold
+    other tensors too).  With `balance` the router's gradient comes too: balance.dlogits
     is that of the output through the routing weights plus that of the balance loss."""
+    opt._check_gradients([(inp["A_gu"], buf.dA_gu), (inp["B_gu"], buf.dB_gu), (inp["A_d"], buf.dA_d),
+                          (inp["B_d"], buf.dB_d)])
     layer_forward(inp, k, scale, buf, stream)
     if balance is not None:
         moe_balance_loss(inp["logits"], buf.ids, balance.loss, balance.counts, balance.n_tokens, balance.ws,

@@ -112,3 +112,37 @@ def test_trained_adapters_served_in_one_batch():
         buf = ml.alloc_buffers(n, cfg.m, cfg.n, 1, 1, cfg.r, cfg.scale)
         ml.layer_forward({**t, "X": X[lo:hi].contiguous(), "logits": torch.zeros(n, 1, device="cuda")}, 1, cfg.scale, buf)
         assert rel_err(to_np(buf.save_GU), to_np(Y[lo:hi])) <= TOL
+
+
+def test_a_step_with_other_gradient_buffers_is_refused():
+    cfg = small_config(T=64, m=64, n=32, E=4, k=2, r=8, alpha=8)
+    inp, _ = inputs_on(cfg)
+    buf, other = (ml.alloc_buffers(cfg.T, cfg.m, cfg.n, cfg.E, cfg.k, cfg.r, cfg.scale) for _ in range(2))
+    grads = lambda b: [b.dA_gu, b.dB_gu, b.dA_d, b.dB_d]      # noqa: E731
+    params = [inp[n] for n in ADAPTERS]
+    for bad in (ml.AdamW(params, grads(other)), ml.AdamW(params, grads(buf)[:3] + grads(other)[3:]),
+                ml.AdamW(params[::-1], [torch.zeros_like(p) for p in params[::-1]]),
+                ml.AdamW([p.clone() for p in params], grads(buf))):
+        before = [p.clone() for p in params]
+        with pytest.raises(ValueError):
+            ml.layer_train_step(inp, cfg.k, cfg.scale, buf, bad)
+        assert int(bad.steps) == 0 and all(torch.equal(a, b) for a, b in zip(before, params))
+    # some of the adapters, in any order, beside another layer's
+    more = torch.zeros(50, device="cuda")
+    opt = ml.AdamW([more, inp["B_d"], inp["A_gu"]], [torch.zeros_like(more), buf.dB_d, buf.dA_gu])
+    ml.layer_train_step(inp, cfg.k, cfg.scale, buf, opt)
+    assert int(opt.steps) == 1
+    # views of separate gate and up adapters
+    ad = ml.SplitGateUpAdapters(cfg.E, cfg.m, cfg.n, cfg.r)
+    for t in (ad.A_g, ad.B_g, ad.A_u, ad.B_u, ad.A_d, ad.B_d):
+        t.normal_(std=0.1)
+    split = ad.layer_inputs(inp)
+    wide = ml.alloc_buffers(cfg.T, cfg.m, cfg.n, cfg.E, cfg.k, 2 * cfg.r, cfg.scale)
+    g = ad.grads(wide)
+    opt = ml.AdamW([ad.A_u, ad.B_u, ad.A_d], [g["dA_u"], g["dB_u"], g["dA_d"]])
+    start = ad.A_u.clone(), ad.A_g.clone()
+    ml.layer_train_step(split, cfg.k, cfg.scale, wide, opt)
+    assert not torch.equal(ad.A_u, start[0]) and torch.equal(ad.A_g, start[1])
+    opt = ml.AdamW([ad.A_u, ad.A_g], [g["dA_g"], g["dA_u"]])
+    with pytest.raises(ValueError):
+        ml.layer_train_step(split, cfg.k, cfg.scale, wide, opt)
