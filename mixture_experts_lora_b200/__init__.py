@@ -472,7 +472,9 @@ class AdamW:
     three dimensions (SplitGateUpAdapters' views).  state_bits: 32 (fp32 moments) or 8 (e4m3
     codes of m and of sqrt(v) with an fp32 scale per 256 elements).  master_weights: an fp32
     copy of every bf16 parameter that the step updates and the parameter is rounded from; without
-    it a change smaller than half a bf16 step of the weight is lost.
+    it a change smaller than half a bf16 step of the weight is lost.  The copies are made at
+    construction: after writing to the parameters (loading weights), call refresh_master(), or the next
+    step puts the old weights back.
 
     lr may be set between steps, or be a device fp32 tensor that captured steps read.  The
     states live in flat tensors, each parameter's part beginning at a multiple of 256 elements
@@ -527,10 +529,10 @@ class AdamW:
             self.exp_avg_sq = torch.zeros(at, dtype=torch.float32, device=dev)
             self.exp_avg_scale = self.exp_avg_sq_scale = None
         self.master = None
-        if any(g[2] for g in groups):
+        self._with_master = [i for g, idx in groups.items() if g[2] for i in idx]
+        if self._with_master:
             self.master = torch.zeros(at, dtype=torch.float32, device=dev)
-            for i in (i for g, idx in groups.items() if g[2] for i in idx):
-                self._part(self.master, i).copy_(self.params[i])
+            self.refresh_master()
         tensors = self.params + self.grads
         self._held = [t.detach() for t in tensors]
         self._looks = [(ts, list(map(_data_ptr, ts)))
@@ -558,6 +560,11 @@ class AdamW:
             cfg = moe_adamw_config_t(0.0, betas[0], betas[1], eps, weight_decay, int(p16), int(g16), int(master),
                                      state_bits)
             self._calls.append((table, len(idx), cfg, ctypes.byref(cfg), int(len(self._calls) == len(groups) - 1)))
+
+    def refresh_master(self):
+        """Takes the master weights anew from the parameters, for weights written to them since."""
+        for i in self._with_master:
+            self._part(self.master, i).copy_(self.params[i])
 
     def _part(self, flat, i):
         p = self.params[i]
@@ -625,7 +632,8 @@ class AdamW:
         return {k: getattr(self, k) for k in self._STATE}
 
     def load_state_dict(self, state: dict):
-        """Copies a state_dict() of an optimizer over the same parameters and settings."""
+        """Copies a state_dict() of an optimizer over the same parameters and settings, the master weights
+        with it; the parameters themselves are loaded apart from it."""
         if any(list(map(_data_ptr, tensors)) != addresses for tensors, addresses in self._looks):
             self._moved()
         for k in self._STATE:

@@ -455,3 +455,25 @@ def test_parameters_that_share_memory_are_refused():
                  (flat[::2], flat[1::2]), (flat[:100].view(torch.bfloat16), flat[100:120]), (flat[5:5], flat[0:10], flat[5:5]),
                  (flat[::4], flat[1::4], flat[2::4], flat[3::4])):
         steps(make_over(*good), n=1)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_master_weights_follow_weights_that_are_loaded(bits):
+    opt = make([(300,), (8, 40)], state_bits=bits, master_weights=True)
+    steps(opt, n=1)
+    for p in opt.params:
+        p.fill_(3.0)
+    opt.refresh_master()
+    for i in range(2):
+        assert (opt._part(opt.master, i) == 3.0).all()
+    steps(opt, n=1)                          # (checked against a step from these weights)
+    for p in opt.params:
+        assert ((p.float() - 3.0).abs() < 0.1).all()
+    mixed = ml.AdamW([torch.ones(9, device="cuda"), torch.ones(9, device="cuda", dtype=BF)],
+                     [torch.ones(9, device="cuda"), torch.ones(9, device="cuda", dtype=BF)], master_weights=True)
+    mixed.params[1].fill_(2.0)
+    mixed.refresh_master()
+    assert (mixed._part(mixed.master, 1) == 2.0).all() and not mixed._part(mixed.master, 0).any()
+    none = make([(5,)], F32, F32)
+    none.refresh_master()                    # nothing to refresh
+    assert none.master is None
