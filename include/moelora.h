@@ -287,7 +287,8 @@ moe_status_t moe_router_backward(const moe_bf16_t* dY, const moe_bf16_t* Y_sorte
  * token_mask  uint8 [T]     (device, read) or NULL (every row counts); rows masked out may
  *             hold any bits
  * loss fp32 [S], counts int32 [S, E], n_tokens int32 [S] = n_s   (device, written)
- * ws, ws_bytes              scratch of at least moe_balance_workspace_bytes(T, E, S)
+ * ws, ws_bytes              scratch of at least moe_balance_workspace_bytes(T, E, S), which grows
+ *             with T and S: what a batch needs does for shorter ones and for fewer sequences
  * An id outside [0, E) in a valid row, or offsets that decrease or leave [0, T], set
  * MOE_ERR_DEVICE_INDEX; the results are then undefined.
  * Supported: k and E as above, 1 <= S < 2^24.  Sums over rows are taken in a fixed order.

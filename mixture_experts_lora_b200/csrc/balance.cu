@@ -649,20 +649,28 @@ moe_status_t check_shape(int64_t T, int32_t E, int32_t k, const int32_t* off, in
   return MOE_OK;
 }
 
+// Slots for any batch of up to T rows: windows get longer where T passes what their number covers, so
+// a shorter batch may have more of them.  (The last summand: nor does it shrink when S grows.)
+int64_t most_slots(int64_t T, int E, int S) {
+  const int64_t blocks = wanted_blocks(E), most = S < blocks / 2 ? blocks + 1 - S : blocks / 2 + 1;
+  const int64_t shortest = (T + 31) / 32;
+  return (shortest < most ? shortest : most) + S;
+}
+
 struct BalanceLayout {
-  int64_t slots, n_win;
+  int64_t n_win;
   size_t psum, pcnt, pn, total;
 };
 BalanceLayout make_layout(int64_t T, int E, int S) {
   BalanceLayout L{};
   const int rows = window_rows(T, E, S);
   L.n_win = (T + rows - 1) / rows;
-  L.slots = L.n_win + S;
-  const size_t row = ((size_t)L.slots * E * 4 + 255) & ~size_t(255);
+  const int64_t slots = most_slots(T, E, S);
+  const size_t row = ((size_t)slots * E * 4 + 255) & ~size_t(255);
   L.psum = 0;
   L.pcnt = row;
   L.pn = 2 * row;
-  L.total = 2 * row + (((size_t)L.slots * 4 + 255) & ~size_t(255));
+  L.total = 2 * row + (((size_t)slots * 4 + 255) & ~size_t(255));
   return L;
 }
 

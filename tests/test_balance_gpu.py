@@ -295,3 +295,22 @@ def test_logits_past_32_bits():
         f[:2] = N
         ref = (f - f.sum() / E) / (k * N * N)
         assert (r - ref).abs().max() <= (3 * E + 64) * U * 2 / (k * N)
+
+
+@pytest.mark.parametrize("E,long,short", [(64, 18945, 18944), (128, 131072, 130832), (300, 9473, 9472), (40, 600, 33)])
+def test_one_workspace_for_batches_of_many_lengths(E, long, short):
+    """The workspace of the longest batch serves shorter ones, and no byte behind it is written."""
+    need = ml.moe_balance_workspace_bytes(long, E, 3)
+    whole = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    for T in (long, short):
+        c = Case(T, E, 2, off=[0, T // 3, T // 2, T], seed=E)
+        x, ids = c.logits.cuda(), c.ids.cuda()
+        off = torch.tensor(c.off, dtype=torch.int32, device="cuda")
+        loss, n = torch.empty(3, device="cuda"), torch.empty(3, dtype=torch.int32, device="cuda")
+        counts = torch.empty(3, E, dtype=torch.int32, device="cuda")
+        ml.moe_balance_loss(x, ids, loss, counts, n, whole[:need], off)
+        torch.cuda.synchronize()
+        assert ml.moe_get_device_error() == ml.MOE_OK
+        rl, rc, rn = O.balance_loss(c.logits.double().numpy(), c.ids.numpy(), 3, c.off, None)
+        assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(n.cpu().numpy(), rn)
+        assert (whole[need:] == 0x5A).all()

@@ -121,3 +121,15 @@ def test_bindings_refuse_cpu_tensors_and_wrong_types():
         ml.AdamW([], [])
     with pytest.raises(ValueError):
         ml.AdamW([z(4)], [z(4)], state_bits=4)
+
+
+@pytest.mark.parametrize("E", [3, 64, 128, 256, 257, 1024])
+@pytest.mark.parametrize("S", [1, 4, 5, 29, 295, 296, 297, 5000])
+def test_a_balance_workspace_for_a_batch_does_for_shorter_ones(L, E, S):
+    rows = sorted({*range(0, 400), *range(400, 140000, 97), *(32 * b + d for b in range(1, 4400) for d in (-1, 0, 1)),
+                   18944, 18945, 130832, 131072, (1 << 31) - 1})
+    need = [ml.moe_balance_workspace_bytes(T, E, S) for T in rows]
+    assert all(a <= b for a, b in zip(need, need[1:]))
+    # nor does a sequence more need less
+    assert all(ml.moe_balance_workspace_bytes(T, E, S) <= ml.moe_balance_workspace_bytes(T, E, S + 1)
+               for T in (0, 1, 40, 1024, 1025, 9000, 18944, 18945, 131071, 1 << 24))
