@@ -477,3 +477,25 @@ def test_master_weights_follow_weights_that_are_loaded(bits):
     none = make([(5,)], F32, F32)
     none.refresh_master()                    # nothing to refresh
     assert none.master is None
+
+
+@pytest.mark.parametrize("sizes,master", [((2200001,), False), ((1500000, 256, 1400300), True), ((11_000_255,), True)])
+def test_8_bit_states_of_large_tensors(sizes, master):
+    """Tensors of which a warp walks several blocks in a row, with a part of a block at the end: codes
+    and scales of two steps from moments that are not zero."""
+    opt = make([(n,) for n in sizes], state_bits=8, master_weights=master)
+    opt.steps.fill_(50)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    for i, (a, n) in enumerate(zip(opt.starts, sizes)):       # (the elements behind a tensor's end stay zero)
+        for codes, top in ((opt.exp_avg, 256), (opt.exp_avg_sq, 128)):
+            draw = torch.randint(0, top, (n,), generator=gen, device="cuda", dtype=torch.int32)
+            codes[a:a + n].view(torch.uint8).copy_(torch.where(draw & 0x7F == 0x7F, draw - 1, draw))
+    opt.exp_avg_scale.copy_(torch.rand(opt.exp_avg_scale.shape, generator=gen, device="cuda") * 1e-4 + 1e-6)
+    opt.exp_avg_sq_scale.copy_(torch.rand(opt.exp_avg_sq_scale.shape, generator=gen, device="cuda") * 1e-4 + 1e-6)
+    steps(opt, n=2)
+
+
+@pytest.mark.parametrize("p,master", [(BF, True), (F32, False)])
+def test_more_elements_than_resident_blocks_take_at_once(p, master):
+    """Over 64 chunks of 2048 elements per SM: the 32-bit step's blocks go on to others."""
+    steps(make([(20_000_003,), (300,)], p, F32, master_weights=master), n=2)

@@ -314,3 +314,18 @@ def test_one_workspace_for_batches_of_many_lengths(E, long, short):
         rl, rc, rn = O.balance_loss(c.logits.double().numpy(), c.ids.numpy(), 3, c.off, None)
         assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(n.cpu().numpy(), rn)
         assert (whole[need:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("T,E,k,cuts", [(60000, 33, 2, ()), (131071, 128, 8, ()), (131071, 128, 8, (40000, 40001, 100000)),
+                                        (100000, 8, 2, ()), (30000, 384, 2, (29000,)), (16384, 1024, 8, ())])
+def test_the_loss_of_long_batches(T, E, k, cuts):
+    """Nothing of a long sum is lost.  A probability is (E + 16) u off.  It is added up over the rows of a
+    window that its warp takes, 32 lanes and 8 warps, and the windows, of which there are at most 592, or 296
+    above 256 experts; then E products.  A lost window would be more than ten times the bound."""
+    c = Case(T, E, k, None if not cuts else [0, *cuts, T], seed=T + E)
+    loss = c.run()[0].double().numpy()
+    ref, _, _ = O.balance_loss(c.logits.double().numpy(), c.ids.numpy(), c.S, c.off, None)
+    windows = 592 if E <= 256 else 296
+    chain = 2 * E + 16 + T // windows + 1 + 5 + 8 + windows + 16
+    assert np.all(np.abs(loss - ref) <= chain * U * ref)
+    assert chain * U < 1 / windows / 10

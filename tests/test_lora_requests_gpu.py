@@ -330,3 +330,10 @@ def test_infinite_rows_follow_the_definition(off, r):
     assert (c.Y[17] == float("inf")).all() and (c.Y[150] == -float("inf")).all()
     rest = [i for i in range(200) if i not in (17, 150)]
     assert torch.isfinite(c.Y[rest]).all()
+
+
+@pytest.mark.parametrize("K,N,r", [(64, 528, 32), (64, 528, 24), (48, 528, 128), (64, 272, 72), (32, 1040, 16), (64, 784, 64)])
+def test_tiles_without_a_cluster(K, N, r):
+    """Up to 64 columns of X a tile is one CTA's, at every padded rank; the columns of Y run through its
+    buffers more than once."""
+    Case(300, K, N, r, 3, [2, 0, 1], [0, 143, 144, 297]).run().check()
