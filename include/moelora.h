@@ -358,7 +358,8 @@ typedef struct {
  * step: device int64 [2]; step[0] is the number of steps taken so far, step[1] is zero between
  * calls.  With advance != 0 the call adds one to step[0] when it is done (several calls that
  * make up one step: the last one advances).  Calls that share `step` must be ordered.
- * No two tensors may share parameter or state memory.  Strided views (size[0] or size[1] > 1)
+ * No two tensors may share parameter or state memory (not checked here); a view whose own elements
+ * meet, a stride below what the dimensions of smaller strides reach, is INVALID_ARG.  Strided views (size[0] or size[1] > 1)
  * hold fewer than 2^31 elements.
  * Alignment: exp_avg, exp_avg_sq, master and step 16 bytes, the others their element's.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */

@@ -16,6 +16,7 @@
 // move as they should although one step changes them by less than a code.
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -576,6 +577,22 @@ cudaError_t launch_all(const moe_adamw_tensor_t* src, int n, const moe_adamw_con
   return cudaGetLastError();
 }
 
+// Whether two elements of the parameter may lie in one place (they would race): a dimension that steps
+// inside the reach of those of smaller strides.
+bool places_meet(const moe_adamw_tensor_t& t) {
+  int by[3] = {0, 1, 2};
+  std::sort(by, by + 3, [&](int a, int b) { return t.param_stride[a] < t.param_stride[b]; });
+  int64_t reach = 1;
+  for (int k : by) {
+    if (t.size[k] <= 1) continue;
+    if (t.param_stride[k] < reach) return true;
+    // (a stride beyond what any memory holds ends the sum before it can overflow)
+    if (t.param_stride[k] > (int64_t(1) << 60) / t.size[k]) return false;
+    reach += t.param_stride[k] * (t.size[k] - 1);
+  }
+  return false;
+}
+
 bool aligned_to(const void* p, size_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
@@ -604,11 +621,10 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int32_
       if (t.size[k] < 0 || t.param_stride[k] < 0 || t.grad_stride[k] < 0) return MOE_ERR_INVALID_ARG;
       if (t.size[k] > (int64_t(1) << 40) || n > (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
       n *= t.size[k];
-      // two elements of one parameter in one place would race
-      if (t.size[k] > 1 && t.param_stride[k] == 0) return MOE_ERR_INVALID_ARG;
     }
     if (n == 0) continue;
     if (n > (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
+    if (places_meet(t)) return MOE_ERR_INVALID_ARG;
     const bool flat = t.size[0] == 1 && t.size[1] == 1 && t.param_stride[2] == 1 && t.grad_stride[2] == 1;
     if (!flat && n >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
     if (!aligned_to(t.param, p16 ? 2 : 4) || !aligned_to(t.grad, g16 ? 2 : 4)) return MOE_ERR_INVALID_ARG;

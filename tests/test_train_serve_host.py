@@ -133,3 +133,9 @@ def test_a_balance_workspace_for_a_batch_does_for_shorter_ones(L, E, S):
     # nor does a sequence more need less
     assert all(ml.moe_balance_workspace_bytes(T, E, S) <= ml.moe_balance_workspace_bytes(T, E, S + 1)
                for T in (0, 1, 40, 1024, 1025, 9000, 18944, 18945, 131071, 1 << 24))
+
+
+def test_adamw_refuses_views_whose_elements_meet(L):
+    for size, stride in (((1, 8, 8), (0, 4, 1)), ((1, 8, 8), (0, 1, 4)), ((9, 8, 8), (8, 64, 1)), ((2, 2, 2), (0, 2, 1)),
+                         ((2, 1, 8), (7, 0, 1)), ((3, 1 << 20, 2), (1 << 20, 2, 1))):
+        assert _adamw(L, size=size, param_stride=stride, grad_stride=stride) == ml.MOE_ERR_INVALID_ARG, (size, stride)
