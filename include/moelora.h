@@ -345,7 +345,7 @@ typedef struct {
 } moe_adamw_tensor_t;
 
 typedef struct {
-  double lr, beta1, beta2, eps, weight_decay;
+  double lr, beta1, beta2, eps, weight_decay;   /* betas in [0, 1); eps 0 or at least 2^-126 */
   int32_t param_bf16;        /* 1: bf16 parameters, 0: fp32; the same for all tensors of a call */
   int32_t grad_bf16;
   int32_t has_master;        /* 1: every tensor has a master weight */

@@ -610,6 +610,8 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int32_
   if (!std::isfinite(c.lr) || !std::isfinite(c.weight_decay) || !(c.eps >= 0) || !std::isfinite(c.eps) ||
       !(c.beta1 >= 0 && c.beta1 < 1) || !(c.beta2 >= 0 && c.beta2 < 1))
     return MOE_ERR_INVALID_ARG;
+  // (the quotient's reciprocal takes a subnormal divisor for zero: 0 / eps would be no number)
+  if (c.eps > 0 && c.eps < 0x1p-126) return MOE_ERR_INVALID_ARG;
   if (c.state_bits != 8 && c.state_bits != 32) return MOE_ERR_UNSUPPORTED;
   const bool p16 = c.param_bf16 != 0, g16 = c.grad_bf16 != 0, master = c.has_master != 0, b8 = c.state_bits == 8;
   if (master && !p16) return MOE_ERR_UNSUPPORTED;

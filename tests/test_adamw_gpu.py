@@ -499,3 +499,18 @@ def test_8_bit_states_of_large_tensors(sizes, master):
 def test_more_elements_than_resident_blocks_take_at_once(p, master):
     """Over 64 chunks of 2048 elements per SM: the 32-bit step's blocks go on to others."""
     steps(make([(20_000_003,), (300,)], p, F32, master_weights=master), n=2)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_the_smallest_eps(bits):
+    """Elements that never had a gradient stay where they are (0 / eps = 0), whatever eps."""
+    p = torch.randn(600, device="cuda")
+    g = torch.zeros(600, device="cuda")
+    g[300] = 1e-3
+    before = p.clone()
+    opt = ml.AdamW([p], [g], lr=0.1, eps=2.0 ** -126, weight_decay=0.0, state_bits=bits)
+    opt.step()
+    moved = (p != before).nonzero().ravel().tolist()
+    assert moved == [300] and torch.isfinite(p).all()
+    with pytest.raises(ml.MoEError):
+        ml.AdamW([p], [g], eps=2.0 ** -127, state_bits=bits).step()

@@ -139,3 +139,8 @@ def test_adamw_refuses_views_whose_elements_meet(L):
     for size, stride in (((1, 8, 8), (0, 4, 1)), ((1, 8, 8), (0, 1, 4)), ((9, 8, 8), (8, 64, 1)), ((2, 2, 2), (0, 2, 1)),
                          ((2, 1, 8), (7, 0, 1)), ((3, 1 << 20, 2), (1 << 20, 2, 1))):
         assert _adamw(L, size=size, param_stride=stride, grad_stride=stride) == ml.MOE_ERR_INVALID_ARG, (size, stride)
+
+
+@pytest.mark.parametrize("eps", [1e-39, 1e-50, 2.0 ** -127])
+def test_adamw_refuses_an_eps_below_the_normal_numbers(L, eps):
+    assert _adamw(L, eps=eps) == ml.MOE_ERR_INVALID_ARG
