@@ -51,6 +51,7 @@ struct AdamwArgs {
   int32_t chunk0[NT + 1];  // first chunk of each tensor
   int n;
   float lr, b1, b2, eps, wd, one_b1, one_b2, ln_b1, ln_b2;
+  float one;               // 1, see update8
   const float* lr_dev;
   const float* grad_scale;
   long long* step;
@@ -144,7 +145,7 @@ __device__ __forceinline__ int64_t view_offset(const Tensor& t, int64_t i, const
 
 // The scalars of a step.
 struct Step {
-  float b1, b2, one_b1, one_b2, eps, gscale, c1, rbc2, keep;
+  float b1, b2, one_b1, one_b2, eps, gscale, c1, rbc2, keep, one;
 };
 
 // One element.  The moments are rounded operation by operation (no fused multiply-adds), as
@@ -159,7 +160,9 @@ __device__ __forceinline__ void weight(const Step& q, float m, float root, float
   w = w * q.keep - q.c1 * (m * rcp_approx(root * q.rbc2 + q.eps));
 }
 
-// Eight elements two at a time: m, v, sqrt(v), w from m, v, g, w.  Returns whether every v is
+// Eight elements two at a time: m, v, sqrt(v), w from m, v, g, w.  The moments' sums are written as
+// x * 1 + y with a 1 that the assembler cannot see: it makes one rounding of a packed product and
+// a packed sum.  Returns whether every v is
 // finite and at least 2^-100.  Their roots are one Newton step (v - s^2) / (2 s) from
 // s = v rsqrt(v): equal to __fsqrt_rn for all 2^24 values of [1, 4), and so for their scalings
 // by 4^k down to 2^-100 (below 2^-102 the bits of v - s^2 leave fp32's range), in half its
@@ -169,13 +172,13 @@ __device__ __forceinline__ bool update8(const Step& q, const float (&g)[8], floa
   const f32x2 b1 = pack2(q.b1, q.b1), b2 = pack2(q.b2, q.b2), o1 = pack2(q.one_b1, q.one_b1),
               o2 = pack2(q.one_b2, q.one_b2), gs = pack2(q.gscale, q.gscale), rb = pack2(q.rbc2, q.rbc2),
               ep = pack2(q.eps, q.eps), kp = pack2(q.keep, q.keep), nc = pack2(-q.c1, -q.c1),
-              mone = pack2(-1.f, -1.f), mhalf = pack2(-0.5f, -0.5f);
+              one = pack2(q.one, q.one), mone = pack2(-1.f, -1.f), mhalf = pack2(-0.5f, -0.5f);
   f32x2 M[4], V[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const f32x2 G = mul2(pack2(g[2 * j], g[2 * j + 1]), gs);
-    M[j] = add2(mul2(b1, pack2(m[2 * j], m[2 * j + 1])), mul2(o1, G));
-    V[j] = add2(mul2(b2, pack2(v[2 * j], v[2 * j + 1])), mul2(o2, mul2(G, G)));
+    M[j] = fma2(mul2(b1, pack2(m[2 * j], m[2 * j + 1])), one, mul2(o1, G));
+    V[j] = fma2(mul2(b2, pack2(v[2 * j], v[2 * j + 1])), one, mul2(o2, mul2(G, G)));
     const float2 x = unpack2(M[j]), y = unpack2(V[j]);
     m[2 * j] = x.x; m[2 * j + 1] = x.y;
     v[2 * j] = y.x; v[2 * j + 1] = y.y;
@@ -410,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 5) adamw_kernel(const __
   // 1 - b^t = -expm1(t ln b): relative accuracy even where b^t is near 1
   const float tf = (float)t_step;
   const Step q = {a.b1, a.b2, a.one_b1, a.one_b2, a.eps, a.grad_scale != nullptr ? *a.grad_scale : 1.0f,
-                  lr / -expm1f(tf * a.ln_b1), 1.0f / sqrtf(-expm1f(tf * a.ln_b2)), 1.0f - lr * a.wd};
+                  lr / -expm1f(tf * a.ln_b1), 1.0f / sqrtf(-expm1f(tf * a.ln_b2)), 1.0f - lr * a.wd,
+                  a.one};
   const uint32_t seed = mix32((uint32_t)t_step);
   const int n_chunks = a.chunk0[a.n], blocks = a.blocks;
   for (int c = blockIdx.x; c < n_chunks; c += gridDim.x) {
@@ -555,6 +559,7 @@ cudaError_t launch(const moe_adamw_tensor_t* src, int n, const moe_adamw_config_
   a.lr = (float)c.lr; a.b1 = (float)c.beta1; a.b2 = (float)c.beta2; a.eps = (float)c.eps;
   a.wd = (float)c.weight_decay;
   a.one_b1 = (float)(1.0 - c.beta1); a.one_b2 = (float)(1.0 - c.beta2);
+  a.one = 1.0f;
   a.ln_b1 = (float)std::log(c.beta1); a.ln_b2 = (float)std::log(c.beta2);
   a.lr_dev = lr; a.grad_scale = gscale;
   a.step = reinterpret_cast<long long*>(step);

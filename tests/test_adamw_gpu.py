@@ -514,3 +514,37 @@ def test_the_smallest_eps(bits):
     assert moved == [300] and torch.isfinite(p).all()
     with pytest.raises(ml.MoEError):
         ml.AdamW([p], [g], eps=2.0 ** -127, state_bits=bits).step()
+
+
+@pytest.mark.parametrize("g", [BF, F32])
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_moments_are_rounded_operation_by_operation(bits, offset, g):
+    """Bit for bit what separate fp32 operations give, in groups of eight and element by element."""
+    n = 256 * 1500 + 40
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    grad = (torch.randn(n + offset, generator=gen, device="cuda") * 1e-3).to(g)[offset:]
+    opt = ml.AdamW([torch.zeros(n + offset, device="cuda")[offset:]], [grad], state_bits=bits, **H)
+    if bits == 32:
+        opt.exp_avg[:n] = torch.randn(n, generator=gen, device="cuda") * 1e-4
+        opt.exp_avg_sq[:n] = (torch.randn(n, generator=gen, device="cuda") * 1e-3).square()
+    else:
+        for codes, top in ((opt.exp_avg, 256), (opt.exp_avg_sq, 128)):
+            draw = torch.randint(0, top, (n,), generator=gen, device="cuda", dtype=torch.int32)
+            codes[:n].view(torch.uint8).copy_(torch.where(draw & 0x7F == 0x7F, draw - 1, draw))
+        opt.exp_avg_scale.copy_(torch.rand(1501, generator=gen, device="cuda") * 1e-6)
+        opt.exp_avg_sq_scale.copy_(torch.rand(1501, generator=gen, device="cuda") * 1e-5)
+    m, v = (x.clone() for x in opt.moments(0))
+    f = lambda x: torch.tensor(x, dtype=F32, device="cuda")      # noqa: E731
+    b1, b2 = H["betas"]
+    x = grad.float()
+    m = torch.add(torch.mul(m, f(b1)), torch.mul(x, f(1 - b1)))
+    v = torch.add(torch.mul(v, f(b2)), torch.mul(torch.mul(x, x), f(1 - b2)))
+    opt.step()
+    if bits == 32:
+        assert torch.equal(opt.exp_avg[:n], m) and torch.equal(opt.exp_avg_sq[:n], v)
+        return
+    inv = f(1.0) / f(448.0)
+    for y, scale in ((m.abs(), opt.exp_avg_scale), (v.sqrt(), opt.exp_avg_sq_scale)):
+        top = torch.nn.functional.pad(y, (0, -n % 256)).view(-1, 256).amax(1)
+        assert torch.equal(scale, top * inv)
