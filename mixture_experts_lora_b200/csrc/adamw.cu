@@ -5,9 +5,10 @@
 //
 // Every element is read and written once: the step is bound by HBM.  The tensors' table
 // travels in the kernel's parameters, so a call needs no copy to the device and a captured
-// call keeps its own table.  Each tensor is cut into chunks of 2048 elements, one block
-// each; a warp owns 256 consecutive elements, which is also the block of elements that
-// shares a scale in 8 bits, so its maximum is a warp reduction.
+// call keeps its own table.  A warp takes 256 consecutive elements at a time, which is also the
+// block of elements that shares a scale in 8 bits, so its maximum is a warp reduction.  Each
+// tensor is cut into chunks of eight warps' work, one such block a warp, in 8 bits up to 32
+// in a row; thread blocks walk the chunks.
 //
 // 8 bits: e4m3 codes of m and of sqrt(v) (the root halves the exponent range that a block
 // has to span), scaled so that the block's largest value is 448.  A code is the value with
@@ -512,11 +513,11 @@ cudaError_t launch(const moe_adamw_tensor_t* src, int n, const moe_adamw_config_
                    const float* gscale, int64_t* step, bool advance, cudaStream_t s) {
   AdamwArgs<NT> a;
   // 8 bits: resident thread blocks that walk chunks of up to 32 blocks a warp, since a chunk's
-  // first block waits for its bytes (eight layers' adapters: 253 us with 8 blocks a warp, 238
-  // with 16, 232 with 32); the length evens out the chunks per thread block.  Not longer than an
-  // average tensor, nor than keeps every SM busy.  32 bits: one block a warp and as many thread
-  // blocks as there are chunks (bound by HBM: 60 us for one layer with master weights, 94% of
-  // the measured copy bandwidth; 66 us as a loop over longer chunks).
+  // first block waits for its bytes (eight layers' adapters, 206 us: 16 blocks a warp 6 us more than
+  // 32, 8 blocks 21 us more); the length evens out the chunks per thread block.  Not longer than an
+  // average tensor, nor than keeps every SM busy.  32 bits: one block a warp and a thread block
+  // for every chunk up to 64 per SM (bound by HBM: 57 us for one layer with master weights, 98% of
+  // the measured copy bandwidth; 6 us more as a loop over longer chunks).
   const int64_t resident = (int64_t)device_sms() * (B8 ? 3 : 64);
   int64_t blocks = 0;
   for (int i = 0; i < n; ++i)

@@ -9,7 +9,7 @@
 //
 // Both directions read every logit once and are bound by HBM (the backward writes as much).
 // Rows are cut into windows; forward a block takes the rows of one sequence in one window (131072 x
-// 128 in 64 sequences: 19.3 us; 22.2 us with a block per window, where one with rows of two
+// 128 in 64 sequences: 18 us; 3 us more with a block per window, where one with rows of two
 // sequences took them one after the other), backward a window.  A row is spread over L lanes (a
 // power of two, 32 from 128 experts on: fewer lanes leave room for several rows in a warp), each
 // holding NQ groups of V experts, V = 4 where rows are 16-byte aligned.  A warp loads U rows per
@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(kThreads, C::N <= 8 ? 4 : 2) balance_partial_k
     px += (int64_t)step * E;
   };
   // pairs per expert, eight ids on their way at a time, the first of them ahead of the logits: the
-  // counting ends while those arrive (131072 x 128, both launches: 23.7 us, 25.4 us with four
-  // ids at a time behind the logits)
+  // counting ends while those arrive (131072 x 128: 1.7 us less than with four ids at a time
+  // behind the logits)
   constexpr int IDS = 8;
   const int pairs = rows * a.k;
   const int32_t* ids = a.ids + r0 * a.k;
@@ -323,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, C::N <= 8 ? 4 : 2) balance_partial_k
 // the cluster's CTAs share the groups and, where there are more CTAs, each group's windows.  A warp
 // sums every so-manyth window, then the CTA's warps and the CTAs are summed, all in a fixed
 // order.  Four windows of a warp are on their way at once, so that up to 1024 windows of 128 experts
-// need one wait for memory (131072 x 128, 592 windows, both launches: 19.9 us, 23.7 us where each of
-// four CTAs took all windows of 32 experts).
+// need one wait for memory (131072 x 128, 592 windows: 3.8 us less than where each of four CTAs took
+// all windows of 32 experts).
 constexpr int kSumThreads = 1024, kGroup = 128, kMaxRanks = 8;
 template <bool V4>
 __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceArgs a) {
@@ -523,8 +523,8 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
       live[u] = live[u] && tu >= s_lo;
       seq[u] = s;
       load_row<C>(px + u * ln.groups * E, E, ln, live[u], v[u]);
-      // what is added to is on its way to L2 meanwhile (131072 x 128 added: 35.8 us, 40.5 us
-      // without; asking for the next rows too took 43 to 46 us)
+      // what is added to is on its way to L2 meanwhile (131072 x 128 added: 36 us, 5 us
+      // more without; asking for the next rows too took 43 to 46 us)
       if (a.accumulate && live[u]) {
 #pragma unroll
         for (int q = 0; q < C::NQ; ++q)
@@ -630,7 +630,8 @@ int rows_for(int64_t T, int64_t blocks) {
   const int64_t per = (T + blocks - 1) / blocks;
   return (int)(per < 32 ? 32 : per);
 }
-// Four blocks per SM, two above 256 experts.
+// Four blocks per SM of 148, two above 256 experts.  (A constant: the workspace's size follows from
+// it and is asked for without a device.)
 int64_t wanted_blocks(int E) { return E <= 256 ? 592 : 296; }
 // Rows per window, forward.  Batches of up to 1024 rows and 32768 logits in few sequences: one window,
 // which needs no second launch.  Otherwise as many (window, sequence) pairs as blocks are wanted

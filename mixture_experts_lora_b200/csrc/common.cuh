@@ -76,8 +76,8 @@ __device__ __forceinline__ float rcp_approx(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// Two fp32 numbers for the packed operations (each rounded as the scalar one is), which issue
-// once for both.
+// Two fp32 numbers for the packed operations, which issue once for both.  Each is rounded as the
+// scalar one is, but the assembler may join a product and the sum that takes it into one rounding.
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pack2(float a, float b) {
   f32x2 r;

@@ -1,8 +1,8 @@
 // Low-rank adapters of many requests beside a shared projection, in place on its output:
 //   Y[t] += c_a (X[t] A_a) B_a,   a the adapter of t's request.
 //
-// Reads X once, the adapters in use once, reads and writes Y once: bound by HBM for long
-// prompts, by latency for a few tokens.  Two forms:
+// Reads X once, reads and writes Y once, and reads a row's or a tile's adapter for each of them (from
+// L2 where several share one): bound by HBM for long prompts, by latency for a few tokens.  Two forms:
 //
 // lora_tiles_kernel, for larger batches of requests of any length.  Rows are cut into windows of 128; a
 // cluster of 1 to 8 CTAs owns the rows of one request within one window and runs both
@@ -12,7 +12,7 @@
 //   2. each CTA receives the partial S of its share of the rows in its shared memory and sums them
 //      in rank order; c S, split into two bf16 (its rounding and what the rounding left), goes to
 //      every CTA as rows of the K-major operand of the second product, K = 2 RP.  Both ways by stores
-//      that count their bytes at the receiver's mbarrier (128 rows, rank 16: 11.8 us, 13.0 us with
+//      that count their bytes at the receiver's mbarrier (128 rows, rank 16: 1.2 us less than with
 //      stores, arrivals and a bulk copy of the operand);
 //   3. each CTA takes its share of the columns, 64 a stage: TMA brings the rows of Y and 64
 //      columns of B, tcgen05.mma forms S B in TMEM, the epilogue warps add it to Y in
@@ -94,7 +94,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
 // the columns.  Both operands stream through one ring of shared-memory slots by bulk copies that
 // one warp issues, so that the memory is busy from the first cycle on and B arrives while the
 // CTAs exchange their sums (registers as buffers held too few bytes: 64 rows at 7168 x 2048, rank
-// 32 took 13.6 us a call where this took 12.3):
+// 32 took 1.3 us more):
 //   * a slot of A is 16 KB of the adapter's share of K rows as they lie, and those rows' x.  A
 //     thread takes 16 bytes (eight ranks of one K row), GP = 2^k >= r / 8 threads side by side
 //     on a K row, so that lanes GP apart hold the same ranks: a warp is summed by shuffles, the
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kSingleThreads) lora_single_kernel(const LoraA
   if (ends(0)) yv = *yp;
   meet();
   // the sums to every CTA, by stores that count their bytes there (64 rows at 7168 x 2048, rank 32:
-  // 9.6 us, 10.3 us with plain stores and a cluster barrier)
+  // 9.5 us, 0.7 us more with plain stores and a cluster barrier)
   if (CL > 1) cluster_wait();
   if (tid == 0 && CL > 1) mbar_arrive_expect_tx(smem_u32(&sm.met), (uint32_t)(CL * r) * 4);
   if (tid < r) {
@@ -372,7 +372,7 @@ struct TilesCfg {
   static constexpr int A_ATOM_BYTES = BK * A_ROWB;
 };
 
-// (Registers are given to warps in fours: two blocks of ten warps hold as many as two of twelve.)
+// (Registers are given to warps in fours: two blocks of eleven warps hold as many as two of twelve.)
 template <class C>
 __global__ void __launch_bounds__((C::THREADS + 127) / 128 * 128, 2)
     lora_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
@@ -798,11 +798,11 @@ cudaError_t launch_tiles(const LoraArgs& a, int CL, cudaStream_t s) {
 
 // CTAs per cluster, 1 to 8: what finishes the tiles soonest if a tile takes 1 / CL and the clusters
 // that run at once are as many as measured: two CTAs per SM up to rank 32, one above, and on 148 SMs
-// places for 33 clusters of four and 15 of eight (3 tiles, 7168 x 4096, rank 32: 14.8 us with 8, 23.2
-// with 4, 40 with 2, 70 us with 1; 20 tiles, rank 64: 38.7 us with 8, 31.0 us with 4).  A last wave of
-// a few clusters costs as much as a full one (rank 64, 35 tiles at 7168 x 4096: 53 us with 2, 61 us
-// with 4), unless two CTAs share an SM, clusters are small and it holds less than a seventh (rank 16,
-// 67 tiles at 2048 x 2048: 25.2 us with 4, 27.0 us with 2, 36.2 us with 1).
+// places for 33 clusters of four and 15 of eight (3 tiles, 7168 x 4096, rank 32: 15.4 us with 8, 23.8
+// with 4, 40 with 2, 70 us with 1; 20 tiles, rank 64: 34.6 us with 8, 26.2 us with 4; 8 tiles, rank 128:
+// 24, 32, 53, 88 us).  A last wave of a few clusters costs as much as a full one (rank 64, 35 tiles at
+// 7168 x 4096: 52 us with 2, 59 us with 4), unless two CTAs share an SM, clusters are small and it holds
+// less than a seventh (rank 16, 67 tiles at 2048 x 2048: 18.3 us with 4, 19.0 with 2, 27.6 us with 1).
 int cluster_size(int64_t T, int S, int K, int r) {
   const double tiles = (double)((T + 127) / 128) + (S - 1);      // (requests cut windows)
   const int per_sm = r <= 32 ? 2 : 1;
@@ -811,7 +811,7 @@ int cluster_size(int64_t T, int S, int K, int r) {
   for (int cl = 1; cl <= 8 && cl <= (K + 63) / 64; cl *= 2) {
     const double places = cl < 4 ? 1. / cl : cl == 4 ? 33. / 148. : 15. / 148.;      // per SM
     const double room = std::floor(device_sms() * places + 1e-6) * per_sm;
-    if (cl == 8 && tiles > room) break;    // (35 tiles, rank 64: 59.8 us)
+    if (cl == 8 && tiles > room) break;    // (35 tiles, rank 64: 60.7 us)
     const double waves = std::ceil(tiles / room - (per_sm == 2 ? 0.15 : 0.));
     const double gain = cl / (waves < 1. ? 1. : waves);
     if (gain > most * 1.1) {               // (a cluster has its own cost)
@@ -833,9 +833,11 @@ bool rows_overlap(const moe_bf16_t* x, int64_t ldx, int64_t K, const moe_bf16_t*
 }
 
 // CTAs per row of lora_single_kernel: 8 while all clusters find a place at once (15 of 8 CTAs),
-// then what keeps the CTAs within two per SM (at 7168 x 2048, rank 32, with 8, 4, 2 and 1: 15 rows
-// 6.2, 7.7, 11.2, 16.9 us; 64 rows 14.4, 10.0, 11.5, 17.0 us; 128 rows 27.7, 18.7, 14.5, 17.3 us;
-// 296 rows 63, 42, 28.2, 23.5 us).
+// then what keeps the CTAs within two per SM (at 7168 x 2048, rank 32, an adapter each, with 8, 4, 2
+// and 1: 15 rows 5.7, 7.0, 10.3, 16.7 us; 64 rows 14.8, 9.5, 10.6, 16.8 us; 128 rows 26.4, 17.8, 14.4,
+// 17.2 us; 296 rows 64, 44, 37, 31.6 us.  The same wins at 2048 x 2048, rank 16, and at 7168 x 4096,
+// rank 128: 61 us with 2 and 67 with 4 for 128 rows; at 512 x 512, rank 8 one CTA does, by 0.3 us at
+// 15 rows and 1.2 us at 128).
 int single_cluster(int64_t rows) {
   if (rows <= 15) return 8;
   int cl = 4;
@@ -844,9 +846,11 @@ int single_cluster(int64_t rows) {
 }
 
 // Rows of a batch of packed requests up to which it is worked through row by row, each row reading
-// its adapter (rows and tiles, us: 15 rows at 7168 x 4096 7.2, 13.5 at rank 32 and 9.8, 15.1 at rank
-// 64; 64 rows 11.5, 13.4 at rank 32 and 17.7, 15.1 at rank 64).  Longer where the requests may be more
-// tiles than clusters of eight find places for (96 rows in 40 requests: 17.2, 24.7 at rank 32).
+// its adapter (rows and tiles, us: 15 rows at 7168 x 4096 6.7, 14.2 at rank 32, 8.8, 15.4 at rank 64 and
+// 14.8, 19.7 at rank 128; 64 rows 10.8, 13.8 at rank 32, 16.8, 15.2 at rank 64 and 30, 20 at rank 128; at
+// 512 x 512 64 rows 5.3, 6.1 at rank 16 and 7.3, 8.8 at rank 64).  Longer where the requests may be more
+// tiles than clusters of eight find places for (96 rows in 40 requests: 16.6, 28.4 at rank 32 and 55, 60
+// at rank 128).
 int few_rows(int S, int r) {
   if (S > (r <= 32 ? 30 : 15)) return 128;
   return r <= 32 ? 64 : 24;
