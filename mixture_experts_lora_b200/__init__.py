@@ -409,7 +409,7 @@ def moe_lora_requests(X, adapters, A, B, scale, Y, seq_offsets=None, stream=None
 
 # ---------------------------------------------------------------- AdamW
 STATE_BLOCK = 256     # elements that share a scale in 8-bit states
-LOOKED_AT = 32        # tensors whose addresses one step compares (50 ns each; a step's own host time is 5 us)
+LOOKED_AT = 16        # tensors whose addresses one step compares (50 ns each; a step's own host time is 5 us)
 _data_ptr = torch.Tensor.data_ptr
 
 
@@ -485,7 +485,7 @@ class AdamW:
     The parameters and gradients must keep their memory, and their sizes and strides, while the
     optimizer is in use: steps, captured ones too, go to the addresses of its construction, whose
     storage it keeps alive.  step() raises ValueError, without a launch, when it sees a tensor that has
-    been given other memory (`p.data = ...`, a module's cast or move); it looks at 32 of them, the next
+    been given other memory (`p.data = ...`, a module's cast or move); it looks at 16 of them, the next
     ones each time where there are more."""
 
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
