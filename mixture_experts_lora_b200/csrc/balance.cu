@@ -18,6 +18,8 @@
 // summed in a fixed order through shared memory, and each (window, sequence) pair writes one
 // partial row; a second launch sums a sequence's partials in a fixed order.  A batch of one
 // window needs no second launch.  Everything is fp32 (counts: integers).
+#include <climits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "sequences.cuh"
@@ -538,16 +540,24 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
         held = seq[u];
         const int n = a.n_tokens[held];
         const float g = a.dloss[held] * loss_factor(E, a.k, n);
-        // counts less their mean: sum_j p_j = 1 lets any constant be taken off the counts, and
-        // small differences keep the digits that counts - sum_j p_j counts_j would cancel
-        const float mean = (float)a.k * (float)n / (float)E;
+        // counts less the least of them: sum_j p_j = 1 lets any constant be taken off the counts, and
+        // small differences keep the digits that counts - sum_j p_j counts_j would cancel.  (Less
+        // their mean, experts without any pair would cancel against it in rows that one expert has:
+        // 2 experts, p = 1.4e-4: 7e-5 of the gradient.)
+        int c[C::N], least = INT_MAX;
 #pragma unroll
         for (int q = 0; q < C::NQ; ++q) {
           const int e = expert_of<C>(ln, q);
 #pragma unroll
-          for (int i = 0; i < C::V; ++i)
-            f[q * C::V + i] = e + i < E ? ((float)a.counts[(int64_t)held * E + e + i] - mean) * g : 0.f;
+          for (int i = 0; i < C::V; ++i) {
+            c[q * C::V + i] = e + i < E ? a.counts[(int64_t)held * E + e + i] : INT_MAX;
+            least = min(least, c[q * C::V + i]);
+          }
         }
+        const uint32_t row = ln.L == 32 ? 0xffffffffu : ((1u << ln.L) - 1) << (ln.group * ln.L);
+        for (int o = ln.L / 2; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(row, least, o));
+#pragma unroll
+        for (int i = 0; i < C::N; ++i) f[i] = c[i] != INT_MAX ? (float)(c[i] - least) * g : 0.f;
       }
       row_exp<C>(v[u], ln);
       float dot = 0.f;

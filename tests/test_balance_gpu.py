@@ -329,3 +329,14 @@ def test_the_loss_of_long_batches(T, E, k, cuts):
     chain = 2 * E + 16 + T // windows + 1 + 5 + 8 + windows + 16
     assert np.all(np.abs(loss - ref) <= chain * U * ref)
     assert chain * U < 1 / windows / 10
+
+
+@pytest.mark.parametrize("T,E,k,off", [(64, 2, 1, None), (132, 1024, 15, [0, 50, 51, 90, 132]), (74, 26, 2, [0, 1, 2, 3, 40, 74]),
+                                       (300, 16, 8, list(range(0, 301, 3))), (3000, 219, 26, [0, 2000, 3000])])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_the_gradient_of_peaked_rows(T, E, k, off, accumulate):
+    """Rows that one expert has nearly whole, beside experts that the sequence never used: the gradient of
+    those is a small probability times a count, and neither cancels."""
+    c = Case(T, E, k, off=off, seed=E, spread=5.0)
+    base = torch.randn(T, E, generator=torch.Generator().manual_seed(9)) * 1e-5 if accumulate else None
+    c.check(c.run(accumulate=base), base)
